@@ -320,22 +320,24 @@ def _plain_product(s, way):
     return {"dgu": _back(s, torch.cat((dg, d * gate * sig), -1), s["out"])}
 
 
-def _shares(t):
-    """|t| over its block's largest, zero where a block is all zeros, and the largest."""
-    a = t.view(-1, STATE_BLOCK).abs()
-    s = a.amax(1)
-    return (a / torch.where(s > 0, s, torch.ones_like(s)).unsqueeze(1)).view(-1), s
+def _scales(t):
+    """The largest |t| of each block (at least the smallest normal number, where it is not zero), and its reciprocal."""
+    s = t.view(-1, STATE_BLOCK).abs().amax(1)
+    s = torch.where(s > 0, s.clamp(min=2.0**-126), s)
+    return s, torch.where(s > 0, 1.0 / s, 0.0)
 
 
 def _encode_m(t):
-    a, s = _shares(t)
-    c = torch.round(torch.sqrt(a) * 127.0)
+    s, inv = _scales(t)
+    share = (t.abs().view(-1, STATE_BLOCK) * inv.unsqueeze(1)).view(-1)
+    c = torch.round(torch.sqrt(share) * 127.0)
     return torch.where(t < 0, -c, c).to(torch.int8), s
 
 
 def _encode_v(t):
-    a, s = _shares(t)
-    c = torch.round(torch.sqrt(torch.sqrt(a)) * 255.0)
+    s, inv = _scales(t)
+    root = (torch.sqrt(t).view(-1, STATE_BLOCK) * torch.sqrt(inv).unsqueeze(1)).view(-1)
+    c = torch.round(torch.sqrt(root) * 255.0)
     return torch.where(t > 0, c.clamp(min=1.0), c).to(torch.uint8), s
 
 
