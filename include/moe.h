@@ -307,6 +307,115 @@ moe_status_t moe_route(const void* x_bf16, const void* w_planes, int64_t T, int6
 moe_status_t moe_pack_mx_scales(const uint8_t* src, int64_t src_ld, uint8_t* dst, int64_t E, int64_t N, int64_t C,
                                 void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training the experts (no counterpart in the PR reports): tokens sorted by
+ * expert and back, the experts' products, an optimizer step, and the
+ * gradients of all of them.  These calls need no context: the caller passes
+ * the arrays.  Rows live in the compact layout of moe_plan_layout (each
+ * expert's rows consecutive from a multiple of 128); rows that carry no token
+ * are neither read nor written.  Row strides (_ld) are in elements.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  MOE_ELEM_BF16 = 0,
+  MOE_ELEM_F32 = 1
+} moe_elem_t;
+
+/* The compact layout of a routing, without a context: topk_ids int32
+ * [T, topk] (-1: no assignment) ->
+ *   counts[e]      int32 [E_local] assignments of local expert e, which is
+ *                  global expert expert_start + e;
+ *   start[e]       int32 [E_local] its first row: the sum of the earlier
+ *                  experts' counts, each rounded up to 128;
+ *   src2dst[t, j]  int32 [T, topk] destination row of assignment (t, j): start
+ *                  plus its rank among the expert's assignments in t * topk + j
+ *                  order; -1 when the assignment is dropped or not local.
+ * Sorted buffers need at most moe_compact_all_tokens(T * topk, E_local, 128)
+ * rows.  ws: device scratch, 16-byte aligned, at least
+ * moe_sort_plan_workspace_size bytes (MOE_ERR_BUFFER_TOO_SMALL otherwise); its
+ * first int32 is the status word (cleared by the call; MOE_ERR_EXPERT_ID for an
+ * id outside [-1, E_global), which is dropped), readable with
+ * moe_read_device_status(ws, ...).  E_local <= 1024, topk <= 64 and fewer than
+ * 2^31 rows (MOE_ERR_UNSUPPORTED otherwise).  int32 arrays: 4-byte aligned. */
+int64_t moe_sort_plan_workspace_size(int64_t T, int32_t topk, int32_t E_local);
+moe_status_t moe_sort_plan(const int32_t* topk_ids, int64_t T, int32_t topk, int32_t E_global, int32_t E_local,
+                           int32_t expert_start, int32_t* src2dst, int32_t* start, int32_t* counts, void* ws,
+                           int64_t ws_bytes, void* stream);
+
+/* Rows to and from the sorted layout, elem (moe_elem_t) bf16 or fp32:
+ *   moe_sort_tokens    sorted[src2dst[t, j], :] = x[t, :]
+ *   moe_unsort_tokens  out[t, :] = sum over j of w[t, j] * sorted[src2dst[t, j], :]
+ *                      (topk_weights fp32 [T, topk]; NULL: w = 1), summed in
+ *                      fp32 in j order, 0 for a token without rows
+ *   moe_unsort_tokens_backward
+ *                      dsorted[src2dst[t, j], :] = w[t, j] * dout[t, :]
+ *                      dweights[t, j] = sum over k of dout[t, k] * sorted[src2dst[t, j], k]
+ *                      in fp32, 0 for a dropped assignment; sorted and dweights
+ *                      may both be NULL (rows' gradient alone)
+ * The gradient of moe_sort_tokens is moe_unsort_tokens without weights.
+ * src2dst entries that are negative or not below rows (the rows of the sorted
+ * buffers) are dropped; each row may be listed once at most.  Results are the
+ * same bits whatever the batch.  Any K >= 1 and any stride >= K; pointers need
+ * the alignment of their elements only, and rows that are whole 16-byte units
+ * are moved as such.  Outputs must not overlap inputs. */
+moe_status_t moe_sort_tokens(const void* x, int64_t x_ld, const int32_t* src2dst, int64_t T, int32_t topk, int64_t K,
+                             int32_t elem, void* sorted, int64_t sorted_ld, int64_t rows, void* stream);
+moe_status_t moe_unsort_tokens(const void* sorted, int64_t sorted_ld, int64_t rows, const int32_t* src2dst,
+                               const float* topk_weights, int64_t T, int32_t topk, int64_t K, int32_t elem, void* out,
+                               int64_t out_ld, void* stream);
+moe_status_t moe_unsort_tokens_backward(const void* dout, int64_t dout_ld, const void* sorted, int64_t sorted_ld,
+                                        int64_t rows, const int32_t* src2dst, const float* topk_weights, int64_t T,
+                                        int32_t topk, int64_t K, int32_t elem, void* dsorted, int64_t dsorted_ld,
+                                        float* dweights, void* stream);
+
+/* One AdamW step over many tensors.  Per element, in fp32:
+ *   g' = grad_scale * g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * param and grad are bf16 or fp32, rounded once when stored (to nearest: a
+ * step smaller than half a bf16 spacing leaves a bf16 param as it was).
+ * master (fp32, for a bf16 param, else NULL) is the value that is stepped;
+ * param is then only written, as its rounding.
+ * state_bits 32: exp_avg and exp_avg_sq are fp32, the scales NULL.
+ * state_bits 8: exp_avg holds int8 codes a and exp_avg_sq uint8 codes b, one
+ * per element; avg_scale and sq_scale fp32 [ceil(n / 256)] one scale s per 256
+ * consecutive elements: m = s a |a| / 127^2, v = s (b / 255)^4.  Each step
+ * sets a block's scales to its largest |m| and v (at least 2^-126 where not 0)
+ * and rounds the roots to the nearest codes, b to at least 1 where v > 0.  All
+ * codes and scales 0 is the state before the first step.  A gradient that is
+ * not finite makes its element of param, and its block's 8-bit states, not
+ * finite.
+ * moe_adamw_create keeps the tensors' pointers (which must stay valid) on the
+ * host and groups them into launches of up to 384 tensors of one combination
+ * of types; moe_adamw_launches says how many a step enqueues.  Pointers need
+ * the alignment of their elements only; arrays that start on a boundary of
+ * four elements are moved in wider accesses.  moe_adamw_step: step counts
+ * from 1; grad_scale is a device fp32 scalar (gradient clipping, loss scaling)
+ * or NULL for 1.  The host-side hyperparameters, step among them, are fixed in
+ * a captured launch. */
+typedef struct moe_adamw moe_adamw;
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* avg_scale;
+  float* sq_scale;
+  float* master;
+  int64_t n;
+  int32_t param_elem;  /* moe_elem_t */
+  int32_t grad_elem;   /* moe_elem_t */
+  int32_t state_bits;  /* 32 or 8 */
+  int32_t reserved;
+} moe_adamw_tensor_t;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+} moe_adamw_hyper_t;
+moe_status_t moe_adamw_create(const moe_adamw_tensor_t* tensors, int32_t count, moe_adamw** out);
+void moe_adamw_destroy(moe_adamw* opt);
+int32_t moe_adamw_launches(const moe_adamw* opt);
+moe_status_t moe_adamw_step(const moe_adamw* opt, const moe_adamw_hyper_t* hyper, const float* grad_scale,
+                            void* stream);
+
 /* Number of kernel launches one moe_forward enqueues (for launch accounting). */
 int32_t moe_forward_launches(const moe_ctx* ctx);
 

@@ -24,6 +24,8 @@ MOE_DTYPE_FP8 = 0
 MOE_DTYPE_BF16 = 1
 MOE_DTYPE_MXFP8 = 2
 MOE_DTYPE_MXFP4 = 3
+MOE_ELEM_BF16 = 0
+MOE_ELEM_F32 = 1
 MOE_LAYOUT_AUTO = 0
 MOE_LAYOUT_COMPACT = 1
 MOE_LAYOUT_MASKED = 2
@@ -66,6 +68,18 @@ class MoeWsLayout(ctypes.Structure):
         ("partial_rows", ctypes.c_int64), ("k_splits1", ctypes.c_int32), ("k_splits2", ctypes.c_int32)]
 
 
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("param", "grad", "exp_avg", "exp_avg_sq", "avg_scale", "sq_scale",
+                                               "master")] + [
+        ("n", ctypes.c_int64), ("param_elem", ctypes.c_int32), ("grad_elem", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MoeAdamwHyper(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libmoe.so is not built ({LIB_PATH}); run python moe_expert_layer_ep_gb300/build.py")
@@ -96,6 +110,15 @@ def _load():
         "moe_route_workspace_size": (I64, [I64, I64, I32]),
         "moe_router_prepare": (I32, [VP, VP, I64, I64, VP]),
         "moe_pack_mx_scales": (I32, [VP, I64, VP, I64, I64, I64, VP]),
+        "moe_sort_plan_workspace_size": (I64, [I64, I32, I32]),
+        "moe_sort_plan": (I32, [VP, I64, I32, I32, I32, I32, VP, VP, VP, VP, I64, VP]),
+        "moe_sort_tokens": (I32, [VP, I64, VP, I64, I32, I64, I32, VP, I64, I64, VP]),
+        "moe_unsort_tokens": (I32, [VP, I64, I64, VP, VP, I64, I32, I64, I32, VP, I64, VP]),
+        "moe_unsort_tokens_backward": (I32, [VP, I64, VP, I64, I64, VP, VP, I64, I32, I64, I32, VP, I64, VP, VP]),
+        "moe_adamw_create": (I32, [P(MoeAdamwTensor), I32, P(VP)]),
+        "moe_adamw_destroy": (None, [VP]),
+        "moe_adamw_launches": (I32, [VP]),
+        "moe_adamw_step": (I32, [VP, P(MoeAdamwHyper), VP, VP]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -111,7 +134,9 @@ EXPORTED = ("moe_compact_all_tokens", "moe_choose_layout", "moe_ctx_create", "mo
             "moe_forward_launches", "moe_read_device_status", "moe_clear_device_status",
             "moe_selftest_wait_timeout", "moe_sf_offset", "moe_strerror", "moe_plan_layout_noalloc",
             "moe_requant_weights_ue8m0", "moe_route", "moe_pack_mx_scales", "moe_route_workspace_size",
-            "moe_router_prepare")
+            "moe_router_prepare", "moe_sort_plan_workspace_size", "moe_sort_plan", "moe_sort_tokens",
+            "moe_unsort_tokens", "moe_unsort_tokens_backward", "moe_adamw_create", "moe_adamw_destroy",
+            "moe_adamw_launches", "moe_adamw_step")
 
 
 def _check(code, what):
@@ -359,6 +384,186 @@ def moe_pack_mx_scales(sf, out=None, stream=None, C=None):
     _require_cuda("out", out, torch.uint8, E * N * (C // 32))
     _check(_lib.moe_pack_mx_scales(_ptr(sf), ld, _ptr(out), E, N, C, _stream(stream)), "moe_pack_mx_scales")
     return out
+
+
+# ------------------------------------------------------------------ training
+_ELEM = {torch.bfloat16: MOE_ELEM_BF16, torch.float32: MOE_ELEM_F32}
+
+
+def _empty(shape, dtype, like, stream):
+    """An output or scratch tensor of a call that runs on stream (None: the current one): memory of the current
+    stream's pool, kept from reuse there until a foreign stream has passed the call."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        t.record_stream(stream)
+    return t
+
+
+def _rows(name, t, dtype=None, cols=None):
+    """A matrix of rows that are contiguous in themselves; returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    ld = t.stride(0)
+    if t.shape[0] > 1 and ld < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap")
+    return ld if ld > t.shape[1] else t.shape[1]
+
+
+def _elem(name, t):
+    try:
+        return _ELEM[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}") from None
+
+
+def moe_sort_plan_workspace_size(T, topk, E_local):
+    return int(_lib.moe_sort_plan_workspace_size(T, topk, E_local))
+
+
+def moe_sort_plan(topk_ids, E_global, E_local=None, expert_start=0, src2dst=None, start=None, counts=None, ws=None,
+                  stream=None):
+    """topk_ids int32 [T, k] -> (src2dst int32 [T, k], start int32 [E_local], counts int32 [E_local]), the compact
+    layout of the routing; see include/moe.h.  ws: uint8 device scratch (allocated here if None) that begins with the
+    status word."""
+    T, topk = topk_ids.shape
+    E_local = E_global if E_local is None else E_local
+    _require_cuda("topk_ids", topk_ids, torch.int32)
+    if src2dst is None:
+        src2dst = _empty((T, topk), torch.int32, topk_ids, stream)
+    if start is None:
+        start = _empty((E_local,), torch.int32, topk_ids, stream)
+    if counts is None:
+        counts = _empty((E_local,), torch.int32, topk_ids, stream)
+    if ws is None:
+        ws = _empty((max(16, moe_sort_plan_workspace_size(T, topk, E_local)),), torch.uint8, topk_ids, stream)
+    _require_cuda("src2dst", src2dst, torch.int32, T * topk)
+    _require_cuda("start", start, torch.int32, E_local)
+    _require_cuda("counts", counts, torch.int32, E_local)
+    _require_cuda("ws", ws, torch.uint8)
+    _check(_lib.moe_sort_plan(_ptr(topk_ids), T, topk, E_global, E_local, expert_start, _ptr(src2dst), _ptr(start),
+                              _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)), "moe_sort_plan")
+    return src2dst, start, counts
+
+
+def moe_sort_tokens(x, src2dst, rows=None, out=None, stream=None):
+    """x [T, K] bf16 or fp32 -> the rows in sorted order [rows, K]; rows that carry no token are left as they are.
+    rows is needed when out is not given (moe_compact_all_tokens)."""
+    T, topk = src2dst.shape
+    K = x.shape[1]
+    x_ld = _rows("x", x)
+    _require_cuda("src2dst", src2dst, torch.int32)
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows, src2dst {T}")
+    if out is None:
+        if rows is None:
+            raise ValueError("rows or out must be given")
+        out = _empty((rows, K), x.dtype, x, stream)
+    _check(_lib.moe_sort_tokens(_ptr(x), x_ld, _ptr(src2dst), T, topk, K, _elem("x", x), _ptr(out),
+                                _rows("out", out, x.dtype, K), out.shape[0], _stream(stream)), "moe_sort_tokens")
+    return out
+
+
+def moe_unsort_tokens(y, src2dst, topk_weights=None, out=None, stream=None):
+    """Sorted rows y [rows, K] -> out [T, K], the (weighted) sum of each token's rows; without weights also the
+    gradient of moe_sort_tokens."""
+    T, topk = src2dst.shape
+    K = y.shape[1]
+    y_ld = _rows("y", y)
+    _require_cuda("src2dst", src2dst, torch.int32)
+    if topk_weights is not None:
+        _require_cuda("topk_weights", topk_weights, torch.float32, T * topk)
+    if out is None:
+        out = _empty((T, K), y.dtype, y, stream)
+    out_ld = _rows("out", out, y.dtype, K)
+    if out.shape[0] != T:
+        raise ValueError(f"out has {out.shape[0]} rows, src2dst {T}")
+    _check(_lib.moe_unsort_tokens(_ptr(y), y_ld, y.shape[0], _ptr(src2dst), _ptr(topk_weights), T, topk, K,
+                                  _elem("y", y), _ptr(out), out_ld, _stream(stream)), "moe_unsort_tokens")
+    return out
+
+
+def moe_unsort_tokens_backward(dout, y, src2dst, topk_weights, dy=None, dw=None, stream=None):
+    """Gradient of moe_unsort_tokens with weights: (dy [rows, K], dw fp32 [T, k]).  dy's rows that carry no token are
+    left as they are."""
+    T, topk = src2dst.shape
+    K = dout.shape[1]
+    dout_ld = _rows("dout", dout)
+    y_ld = _rows("y", y, dout.dtype, K)
+    _require_cuda("src2dst", src2dst, torch.int32)
+    _require_cuda("topk_weights", topk_weights, torch.float32, T * topk)
+    if dout.shape[0] != T:
+        raise ValueError(f"dout has {dout.shape[0]} rows, src2dst {T}")
+    if dy is None:
+        dy = _empty(tuple(y.shape), y.dtype, y, stream)
+    if dw is None:
+        dw = _empty((T, topk), torch.float32, y, stream)
+    dy_ld = _rows("dy", dy, dout.dtype, K)
+    _require_cuda("dw", dw, torch.float32, T * topk)
+    if dy.shape[0] != y.shape[0]:
+        raise ValueError(f"dy has {dy.shape[0]} rows, y {y.shape[0]}")
+    _check(_lib.moe_unsort_tokens_backward(_ptr(dout), dout_ld, _ptr(y), y_ld, y.shape[0], _ptr(src2dst),
+                                           _ptr(topk_weights), T, topk, K, _elem("dout", dout), _ptr(dy), dy_ld,
+                                           _ptr(dw), _stream(stream)), "moe_unsort_tokens_backward")
+    return dy, dw
+
+
+class MoeAdamw:
+    """Owns one moe_adamw (the tensors of an optimizer step); see include/moe.h."""
+
+    def __init__(self, handle, tensors):
+        self.handle = handle
+        self._tensors = tensors   # keep them alive with the handle
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:
+            _lib.moe_adamw_destroy(h)
+
+
+def moe_adamw_create(params, grads, exp_avgs, exp_avg_sqs, masters=None, avg_scales=None, sq_scales=None):
+    """Lists of CUDA tensors, one entry per parameter.  States float32, or int8 (exp_avgs) and uint8 (exp_avg_sqs)
+    with float32 scales of ceil(n / 256) elements.  masters: float32 copies of bf16 params (entries may be None)."""
+    n = len(params)
+    none = [None] * n
+    lists = [params, grads, exp_avgs, exp_avg_sqs, avg_scales or none, sq_scales or none, masters or none]
+    if any(len(x) != n for x in lists):
+        raise ValueError("moe_adamw_create: lists of different lengths")
+    table = (MoeAdamwTensor * max(1, n))()
+    for i, (p, g, m, v, ms, vs, w) in enumerate(zip(*lists)):
+        k, blocks = p.numel(), -(-p.numel() // 256)
+        bits = 32 if m.dtype == torch.float32 else 8
+        _require_cuda(f"params[{i}]", p)
+        _require_cuda(f"grads[{i}]", g, None, k)
+        _require_cuda(f"exp_avgs[{i}]", m, torch.float32 if bits == 32 else torch.int8, k)
+        _require_cuda(f"exp_avg_sqs[{i}]", v, torch.float32 if bits == 32 else torch.uint8, k)
+        for name, t, numel in (("avg_scales", ms, blocks), ("sq_scales", vs, blocks), ("masters", w, k)):
+            if t is not None:
+                _require_cuda(f"{name}[{i}]", t, torch.float32, numel)
+        table[i] = MoeAdamwTensor(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(ms), _ptr(vs), _ptr(w), k,
+                                  _elem(f"params[{i}]", p), _elem(f"grads[{i}]", g), bits, 0)
+    h = ctypes.c_void_p()
+    _check(_lib.moe_adamw_create(table, n, ctypes.byref(h)), "moe_adamw_create")
+    return MoeAdamw(h, lists)
+
+
+def moe_adamw_launches(opt):
+    return int(_lib.moe_adamw_launches(opt.handle))
+
+
+def moe_adamw_step(opt, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=None, stream=None):
+    """One step (step counts from 1).  grad_scale: float32 CUDA scalar that multiplies every gradient."""
+    if grad_scale is not None:
+        _require_cuda("grad_scale", grad_scale, torch.float32, 1)
+    h = MoeAdamwHyper(lr, beta1, beta2, eps, weight_decay, step)
+    _check(_lib.moe_adamw_step(opt.handle, ctypes.byref(h), _ptr(grad_scale), _stream(stream)), "moe_adamw_step")
 
 
 def ws_view(ctx, ws, name):

@@ -73,9 +73,9 @@ struct PlanArgs {
   int32_t* padded;
   int32_t* start;
   int32_t* masked_m;
-  int32_t* m_indices;
+  int32_t* m_indices;       // optional (compact)
   int32_t* src2dst;
-  int32_t* block_info;      // int4 per block
+  int32_t* block_info;      // optional: int4 per block
   int32_t* chunk_hist;      // [E_local, chunks]
   int32_t* chunk_rank;      // [A]
   int32_t* block_vrow;      // masked, optional: [blocks] first valid-row index of each block

@@ -140,7 +140,7 @@ __device__ void expert_tables(const PlanArgs& p, const int* s_count, int* s_warp
         // sum of the earlier experts' valid rows
         if (p.block_vrow) p.block_vrow[blk_start + b] = row_start + b * kBlockM;
       }
-      reinterpret_cast<int4*>(p.block_info)[blk_start + b] = info;
+      if (p.block_info) reinterpret_cast<int4*>(p.block_info)[blk_start + b] = info;
     }
   }
   if (threadIdx.x == 0) {
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256) plan_finalize(PlanArgs p) {
     }
     p.src2dst[i] = dst;
   }
-  if (!p.masked)
+  if (!p.masked && p.m_indices)
     fill_m_indices(p, s_tab, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, stride);
 }
 
@@ -331,7 +331,7 @@ __device__ void plan_small_body(const PlanArgs& p) {
     }
     p.src2dst[i] = dst;
   }
-  if (!p.masked) fill_m_indices(p, s_tab, tid, 1024);
+  if (!p.masked && p.m_indices) fill_m_indices(p, s_tab, tid, 1024);
 }
 
 __global__ void __launch_bounds__(1024) plan_small(PlanArgs p) {

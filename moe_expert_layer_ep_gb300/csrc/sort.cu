@@ -1,0 +1,406 @@
+// Tokens sorted by expert and back, and the gradients of both ways
+// (moe_sort_plan, moe_sort_tokens, moe_unsort_tokens,
+// moe_unsort_tokens_backward).  No counterpart in the PR reports: the layer's
+// quant-scatter and combine are bound to a context's weights, dtype and
+// workspace and have no gradient; these work on any rows.
+//
+//   sort      xs[src2dst[t, j]] = x[t]
+//   unsort    out[t] = sum_j w[t, j] * y[src2dst[t, j]]      (w absent: 1)
+//   backward of sort    dx[t] = sum_j dxs[src2dst[t, j]]     = unsort without w
+//   backward of unsort  dy[src2dst[t, j]] = w[t, j] * dout[t]
+//                       dw[t, j] = <dout[t], y[src2dst[t, j]]>
+//
+// All of them are bound by the bytes of the rows.  A group of threads owns one
+// token and walks its columns, so the token's own row is read or written once
+// whatever topk is, every sorted row once, and sums over j are taken in j
+// order in fp32 registers: nothing is added atomically, the results are the
+// same bits every time and at every batch size.
+#include <string.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSortThreads = 256;
+constexpr int kSortBatch = 4;     // row segments a thread has in flight
+constexpr int kJBatch = 8;        // selections handled together
+
+struct SortArgs {
+  const void* x;            // sort: x; unsort: sorted rows; backward: dout
+  const void* y;            // backward: sorted rows of the forward (NULL: no dw)
+  const int32_t* src2dst;   // [T, topk]
+  const float* w;           // [T, topk] or NULL
+  void* out;                // sort: sorted rows; unsort: out; backward: dy
+  float* dw;                // backward
+  int64_t T, K, rows;
+  int64_t x_ld, y_ld, out_ld;   // elements
+  int32_t topk;
+  int32_t lanes_log2;       // log2 of the threads that share a token
+};
+
+// A thread's share of a row: kVec consecutive elements, as one access.
+template <typename E, int kVec>
+struct Pack;
+template <>
+struct Pack<uint16_t, 8> {
+  using Raw = uint4;
+  __device__ static void open(const Raw& r, float (&f)[8]) {
+    const float2 a = unpack_bf16x2(r.x), b = unpack_bf16x2(r.y), c = unpack_bf16x2(r.z), d = unpack_bf16x2(r.w);
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y; f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
+  }
+  __device__ static Raw close(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Pack<uint16_t, 1> {
+  using Raw = uint16_t;
+  __device__ static void open(const Raw& r, float (&f)[1]) { f[0] = __uint_as_float(static_cast<uint32_t>(r) << 16); }
+  __device__ static Raw close(const float (&f)[1]) { return __bfloat16_as_ushort(__float2bfloat16_rn(f[0])); }
+};
+template <>
+struct Pack<float, 4> {
+  using Raw = float4;
+  __device__ static void open(const Raw& r, float (&f)[4]) { f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w; }
+  __device__ static Raw close(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Pack<float, 1> {
+  using Raw = float;
+  __device__ static void open(const Raw& r, float (&f)[1]) { f[0] = r; }
+  __device__ static Raw close(const float (&f)[1]) { return f[0]; }
+};
+
+// Destination row of selection j of token t, -1 when there is none (dropped,
+// or outside the sorted buffer).
+__device__ __forceinline__ int64_t dest(const SortArgs& a, int64_t t, int j) {
+  if (j >= a.topk) return -1;
+  const int64_t d = a.src2dst[t * a.topk + j];
+  return d < a.rows ? d : -1;
+}
+
+template <typename E, int kVec>
+__global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(SortArgs a) {
+  using P = Pack<E, kVec>;
+  using Raw = typename P::Raw;
+  const int lanes = 1 << a.lanes_log2;
+  const int lane = threadIdx.x & (lanes - 1);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+  pdl_wait();
+  pdl_trigger();
+  if (t >= a.T) return;
+  const E* xrow = static_cast<const E*>(a.x) + t * a.x_ld;
+  E* out = static_cast<E*>(a.out);
+  const int64_t step = static_cast<int64_t>(lanes) * kVec;
+  for (int64_t c0 = static_cast<int64_t>(lane) * kVec; c0 < a.K; c0 += kSortBatch * step) {
+    Raw v[kSortBatch];
+#pragma unroll
+    for (int b = 0; b < kSortBatch; ++b)
+      if (c0 + b * step < a.K) v[b] = *reinterpret_cast<const Raw*>(xrow + c0 + b * step);
+    for (int j = 0; j < a.topk; ++j) {
+      const int64_t d = dest(a, t, j);
+      if (d < 0) continue;
+      E* orow = out + d * a.out_ld + c0;
+#pragma unroll
+      for (int b = 0; b < kSortBatch; ++b)
+        if (c0 + b * step < a.K) *reinterpret_cast<Raw*>(orow + b * step) = v[b];
+    }
+  }
+}
+
+template <typename E, int kVec>
+__global__ void __launch_bounds__(kSortThreads) unsort_tokens_kernel(SortArgs a) {
+  using P = Pack<E, kVec>;
+  using Raw = typename P::Raw;
+  const int lanes = 1 << a.lanes_log2;
+  const int lane = threadIdx.x & (lanes - 1);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+  pdl_wait();
+  pdl_trigger();
+  if (t >= a.T) return;
+  const E* y = static_cast<const E*>(a.x);
+  E* orow = static_cast<E*>(a.out) + t * a.out_ld;
+  for (int64_t c = static_cast<int64_t>(lane) * kVec; c < a.K; c += static_cast<int64_t>(lanes) * kVec) {
+    float acc[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < a.topk; j0 += kJBatch) {
+      Raw v[kJBatch];
+      int64_t d[kJBatch];
+#pragma unroll
+      for (int jj = 0; jj < kJBatch; ++jj) {
+        d[jj] = dest(a, t, j0 + jj);
+        if (d[jj] >= 0) v[jj] = *reinterpret_cast<const Raw*>(y + d[jj] * a.x_ld + c);
+      }
+#pragma unroll
+      for (int jj = 0; jj < kJBatch; ++jj) {
+        if (d[jj] < 0) continue;
+        const float w = a.w ? a.w[t * a.topk + j0 + jj] : 1.0f;
+        float f[kVec];
+        P::open(v[jj], f);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      }
+    }
+    *reinterpret_cast<Raw*>(orow + c) = P::close(acc);
+  }
+}
+
+template <typename E, int kVec>
+__global__ void __launch_bounds__(kSortThreads) unsort_backward_kernel(SortArgs a) {
+  using P = Pack<E, kVec>;
+  using Raw = typename P::Raw;
+  __shared__ float s_dot[kSortThreads / 32][kJBatch];
+  const int lanes = 1 << a.lanes_log2;
+  const int lane = threadIdx.x & (lanes - 1), warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+  pdl_wait();
+  pdl_trigger();
+  const bool live = t < a.T;
+  const E* drow = static_cast<const E*>(a.x) + t * a.x_ld;
+  const E* y = static_cast<const E*>(a.y);
+  E* dy = static_cast<E*>(a.out);
+  for (int j0 = 0; j0 < a.topk; j0 += kJBatch) {
+    int64_t d[kJBatch];
+    float w[kJBatch], dot[kJBatch];
+#pragma unroll
+    for (int jj = 0; jj < kJBatch; ++jj) {
+      d[jj] = live ? dest(a, t, j0 + jj) : -1;
+      w[jj] = d[jj] >= 0 ? a.w[t * a.topk + j0 + jj] : 0.0f;
+      dot[jj] = 0.0f;
+    }
+    for (int64_t c = static_cast<int64_t>(lane) * kVec; live && c < a.K; c += static_cast<int64_t>(lanes) * kVec) {
+      const Raw rd = *reinterpret_cast<const Raw*>(drow + c);
+      Raw v[kJBatch];
+      if (y) {
+#pragma unroll
+        for (int jj = 0; jj < kJBatch; ++jj)
+          if (d[jj] >= 0) v[jj] = *reinterpret_cast<const Raw*>(y + d[jj] * a.y_ld + c);
+      }
+      float g[kVec];
+      P::open(rd, g);
+#pragma unroll
+      for (int jj = 0; jj < kJBatch; ++jj) {
+        if (d[jj] < 0) continue;
+        float f[kVec];
+        if (y) {
+          P::open(v[jj], f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) dot[jj] = fmaf(g[i], f[i], dot[jj]);
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) f[i] = w[jj] * g[i];
+        *reinterpret_cast<Raw*>(dy + d[jj] * a.out_ld + c) = P::close(f);
+      }
+    }
+    if (!y) continue;
+#pragma unroll
+    for (int jj = 0; jj < kJBatch; ++jj)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot[jj] += __shfl_xor_sync(0xFFFFFFFFu, dot[jj], o);
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int jj = 0; jj < kJBatch; ++jj) s_dot[warp][jj] = dot[jj];
+    }
+    __syncthreads();
+    // the group's first threads add its warps' sums in order
+    if (live && lane < kJBatch && j0 + lane < a.topk) {
+      float sum = 0.0f;
+      for (int k = 0; k < lanes / 32; ++k) sum += s_dot[warp + k][lane];
+      a.dw[t * a.topk + j0 + lane] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+using SortKernel = void (*)(SortArgs);
+enum SortOp { kOpSort, kOpUnsort, kOpBackward };
+
+template <typename E, int kVec>
+SortKernel kernel_of(SortOp op) {
+  if (op == kOpSort) return sort_tokens_kernel<E, kVec>;
+  return op == kOpUnsort ? unsort_tokens_kernel<E, kVec> : unsort_backward_kernel<E, kVec>;
+}
+
+// Row accesses are 16 bytes wide when every row starts on a 16-byte boundary
+// and its length is a multiple of 16 bytes, else one element wide.
+moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
+  if (a.T == 0) return MOE_OK;
+  const int es = elem == MOE_ELEM_F32 ? 4 : 2, wide = 16 / es;
+  const bool has_y = a.y != nullptr;
+  const uintptr_t bases = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) |
+                          (has_y ? reinterpret_cast<uintptr_t>(a.y) : 0);
+  const bool vec = bases % 16 == 0 && a.K % wide == 0 && a.x_ld % wide == 0 && a.out_ld % wide == 0 &&
+                   (!has_y || a.y_ld % wide == 0);
+  const int64_t units = vec ? a.K / wide : a.K;
+  a.lanes_log2 = 5;
+  while (a.lanes_log2 < 8 && (int64_t(1) << a.lanes_log2) < units) ++a.lanes_log2;
+  const int64_t per_cta = kSortThreads >> a.lanes_log2;
+  const int64_t grid = (a.T + per_cta - 1) / per_cta;
+  SortKernel k;
+  if (elem == MOE_ELEM_F32)
+    k = vec ? kernel_of<float, 4>(op) : kernel_of<float, 1>(op);
+  else
+    k = vec ? kernel_of<uint16_t, 8>(op) : kernel_of<uint16_t, 1>(op);
+  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(kSortThreads), 0, s, a) == cudaSuccess ? MOE_OK
+                                                                                                 : MOE_ERR_CUDA;
+}
+
+bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Checks that the three row operators share.
+moe_status_t check_sort(int64_t T, int32_t topk, int64_t K, int32_t elem, int64_t rows, const int32_t* src2dst,
+                        const void* tokens, int64_t tokens_ld, const void* sorted, int64_t sorted_ld) {
+  if (T < 0 || topk <= 0 || K <= 0 || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (elem != MOE_ELEM_BF16 && elem != MOE_ELEM_F32) return MOE_ERR_INVALID_ARG;
+  if (tokens_ld < K || sorted_ld < K) return MOE_ERR_INVALID_ARG;
+  if (topk > kMaxTopk || T > 0x7FFFFFFF || rows > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!src2dst || !tokens || (!sorted && rows > 0)) return MOE_ERR_INVALID_ARG;
+  const uintptr_t es = elem == MOE_ELEM_F32 ? 4 : 2;
+  if (off(src2dst, 4) || off(tokens, es) || off(sorted, es)) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
+
+struct SortWs {
+  uint64_t meta, padded, hist, rank, total;
+  int64_t chunks;
+};
+SortWs sort_ws(int64_t A, int32_t E) {
+  SortWs w;
+  w.chunks = (A + kPlanChunk - 1) / kPlanChunk;
+  w.meta = 256;   // the status word comes first
+  w.padded = w.meta + 256;
+  w.hist = w.padded + align256(4 * static_cast<uint64_t>(E));
+  w.rank = w.hist + align256(4 * static_cast<uint64_t>(w.chunks) * E);
+  w.total = w.rank + align256(4 * static_cast<uint64_t>(A));
+  return w;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+extern "C" {
+
+int64_t moe_sort_plan_workspace_size(int64_t T, int32_t topk, int32_t E_local) {
+  if (T < 0 || topk <= 0 || E_local <= 0 || T >= (int64_t(1) << 31)) return -1;
+  return static_cast<int64_t>(moe::sort_ws(T * topk, E_local).total);
+}
+
+moe_status_t moe_sort_plan(const int32_t* topk_ids, int64_t T, int32_t topk, int32_t E_global, int32_t E_local,
+                           int32_t expert_start, int32_t* src2dst, int32_t* start, int32_t* counts, void* ws,
+                           int64_t ws_bytes, void* stream) {
+  if (T < 0 || topk <= 0 || E_global <= 0 || E_local <= 0 || expert_start < 0 ||
+      static_cast<int64_t>(E_local) + expert_start > E_global)
+    return MOE_ERR_INVALID_ARG;
+  if (E_local > moe::kMaxLocalExperts || topk > moe::kMaxTopk || T >= (int64_t(1) << 31) ||
+      moe_compact_all_tokens(T * topk, E_local, 128) >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if ((T > 0 && (!topk_ids || !src2dst)) || !start || !counts || !ws) return MOE_ERR_INVALID_ARG;
+  if (moe::off(topk_ids, 4) || moe::off(src2dst, 4) || moe::off(start, 4) || moe::off(counts, 4) || moe::off(ws, 16))
+    return MOE_ERR_MISALIGNED;
+  const int64_t A = T * topk;
+  const moe::SortWs w = moe::sort_ws(A, E_local);
+  if (ws_bytes < static_cast<int64_t>(w.total)) return MOE_ERR_BUFFER_TOO_SMALL;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  moe::PlanArgs p;
+  memset(&p, 0, sizeof(p));
+  p.topk_ids = topk_ids;
+  p.A = A;
+  p.E_global = E_global;
+  p.E_local = E_local;
+  p.expert_start = expert_start;
+  p.chunks = static_cast<int32_t>(w.chunks);
+  p.status = reinterpret_cast<int32_t*>(base);
+  p.meta = reinterpret_cast<int32_t*>(base + w.meta);
+  p.counts = counts;
+  p.padded = reinterpret_cast<int32_t*>(base + w.padded);
+  p.start = start;
+  p.src2dst = src2dst;
+  p.chunk_hist = reinterpret_cast<int32_t*>(base + w.hist);
+  p.chunk_rank = reinterpret_cast<int32_t*>(base + w.rank);
+  return moe::launch_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_sort_tokens(const void* x, int64_t x_ld, const int32_t* src2dst, int64_t T, int32_t topk, int64_t K,
+                             int32_t elem, void* sorted, int64_t sorted_ld, int64_t rows, void* stream) {
+  const moe_status_t st = moe::check_sort(T, topk, K, elem, rows, src2dst, x, x_ld, sorted, sorted_ld);
+  if (st != MOE_OK) return st;
+  moe::SortArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.x_ld = x_ld;
+  a.src2dst = src2dst;
+  a.T = T;
+  a.K = K;
+  a.topk = topk;
+  a.rows = rows;
+  a.out = sorted;
+  a.out_ld = sorted_ld;
+  return moe::launch_sort(moe::kOpSort, a, elem, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_unsort_tokens(const void* sorted, int64_t sorted_ld, int64_t rows, const int32_t* src2dst,
+                               const float* topk_weights, int64_t T, int32_t topk, int64_t K, int32_t elem, void* out,
+                               int64_t out_ld, void* stream) {
+  const moe_status_t st = moe::check_sort(T, topk, K, elem, rows, src2dst, out, out_ld, sorted, sorted_ld);
+  if (st != MOE_OK) return st;
+  if (moe::off(topk_weights, 4)) return MOE_ERR_MISALIGNED;
+  moe::SortArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = sorted;
+  a.x_ld = sorted_ld;
+  a.src2dst = src2dst;
+  a.w = topk_weights;
+  a.T = T;
+  a.K = K;
+  a.topk = topk;
+  a.rows = rows;
+  a.out = out;
+  a.out_ld = out_ld;
+  return moe::launch_sort(moe::kOpUnsort, a, elem, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_unsort_tokens_backward(const void* dout, int64_t dout_ld, const void* sorted, int64_t sorted_ld,
+                                        int64_t rows, const int32_t* src2dst, const float* topk_weights, int64_t T,
+                                        int32_t topk, int64_t K, int32_t elem, void* dsorted, int64_t dsorted_ld,
+                                        float* dweights, void* stream) {
+  moe_status_t st = moe::check_sort(T, topk, K, elem, rows, src2dst, dout, dout_ld, dsorted, dsorted_ld);
+  if (st != MOE_OK) return st;
+  if ((sorted == nullptr) != (dweights == nullptr) && rows > 0) return MOE_ERR_INVALID_ARG;
+  if (sorted && sorted_ld < K) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && !topk_weights) return MOE_ERR_INVALID_ARG;
+  if (moe::off(topk_weights, 4) || moe::off(dweights, 4) || moe::off(sorted, elem == MOE_ELEM_F32 ? 4 : 2))
+    return MOE_ERR_MISALIGNED;
+  if (rows == 0) {   // nothing was kept: no rows, and every weight's gradient is 0
+    if (T == 0 || !dweights) return MOE_OK;
+    return cudaMemsetAsync(dweights, 0, sizeof(float) * T * topk, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+  }
+  moe::SortArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = dout;
+  a.x_ld = dout_ld;
+  a.y = sorted;
+  a.y_ld = sorted_ld;
+  a.src2dst = src2dst;
+  a.w = topk_weights;
+  a.T = T;
+  a.K = K;
+  a.topk = topk;
+  a.rows = rows;
+  a.out = dsorted;
+  a.out_ld = dsorted_ld;
+  a.dw = dweights;
+  return moe::launch_sort(moe::kOpBackward, a, elem, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
