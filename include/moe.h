@@ -367,6 +367,45 @@ moe_status_t moe_unsort_tokens_backward(const void* dout, int64_t dout_ld, const
                                         int32_t topk, int64_t K, int32_t elem, void* dsorted, int64_t dsorted_ld,
                                         float* dweights, void* stream);
 
+/* The experts' products on sorted rows and their gradients.  Expert e's rows
+ * are counts[e] consecutive rows from start[e] (int32 [E], device, as
+ * moe_sort_plan or moe_plan_layout writes them; any start that keeps the rows
+ * inside the buffers will do).  bf16 in and out, fp32 sums, one rounding:
+ *   moe_expert_gemm               y[r] = x[r] W_e^T               w [E, N, C]
+ *   moe_expert_gemm_swiglu        g | u = x[r] W13_e^T, h[r] = silu(g) * u of the
+ *                                 unrounded g, u                  w13 [E, 2I, C]
+ *                                 gu [rows, 2I] (g, then u) for the gradient, or
+ *                                 NULL where none is wanted
+ *   moe_expert_gemm_dgrad         dx[r] = dy[r] W_e               w [E, N, C]
+ *   moe_expert_gemm_dgrad_swiglu  dh = dy[r] W2_e;  with s = 1 / (1 + exp(-g)):
+ *                                 dgu = dh u s (1 + g (1 - s)) | dh g s
+ *                                 w2 [E, N, I], gu as the forward stored it
+ *   moe_expert_gemm_wgrad         dw[e] = sum over e's rows of dy[r]^T x[r]
+ *                                 dw [E, N, C]; zeros for an expert without rows
+ * Rows outside all experts are neither read into a result nor written, whatever
+ * they hold.  A row's results are the same bits whatever the other rows are;
+ * all results are the same bits every time.  N, I, C and row strides must be
+ * multiples of 8, E <= 1024, rows < 2^31 (MOE_ERR_UNSUPPORTED otherwise);
+ * matrices 16-byte aligned (MOE_ERR_MISALIGNED).  status: device int32, not
+ * cleared here, set where 0 to MOE_ERR_INVALID_ARG when an expert's numbers do
+ * not fit the buffers (that expert is left out) or to MOE_ERR_TIMEOUT; the
+ * workspace of moe_sort_plan can serve (moe_read_device_status reads it). */
+moe_status_t moe_expert_gemm(const void* x, int64_t x_ld, int64_t rows, const void* w, const int32_t* start,
+                             const int32_t* counts, int32_t E, int64_t N, int64_t C, void* y, int64_t y_ld,
+                             void* status, void* stream);
+moe_status_t moe_expert_gemm_swiglu(const void* x, int64_t x_ld, int64_t rows, const void* w13, const int32_t* start,
+                                    const int32_t* counts, int32_t E, int64_t I, int64_t C, void* gu, int64_t gu_ld,
+                                    void* h, int64_t h_ld, void* status, void* stream);
+moe_status_t moe_expert_gemm_dgrad(const void* dy, int64_t dy_ld, int64_t rows, const void* w, const int32_t* start,
+                                   const int32_t* counts, int32_t E, int64_t N, int64_t C, void* dx, int64_t dx_ld,
+                                   void* status, void* stream);
+moe_status_t moe_expert_gemm_dgrad_swiglu(const void* dy, int64_t dy_ld, int64_t rows, const void* w2, const void* gu,
+                                          int64_t gu_ld, const int32_t* start, const int32_t* counts, int32_t E,
+                                          int64_t N, int64_t I, void* dgu, int64_t dgu_ld, void* status, void* stream);
+moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, int64_t rows,
+                                   const int32_t* start, const int32_t* counts, int32_t E, int64_t N, int64_t C,
+                                   void* dw, void* status, void* stream);
+
 /* One AdamW step over many tensors.  Per element, in fp32:
  *   g' = grad_scale * g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)

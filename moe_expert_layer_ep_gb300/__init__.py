@@ -115,6 +115,11 @@ def _load():
         "moe_sort_tokens": (I32, [VP, I64, VP, I64, I32, I64, I32, VP, I64, I64, VP]),
         "moe_unsort_tokens": (I32, [VP, I64, I64, VP, VP, I64, I32, I64, I32, VP, I64, VP]),
         "moe_unsort_tokens_backward": (I32, [VP, I64, VP, I64, I64, VP, VP, I64, I32, I64, I32, VP, I64, VP, VP]),
+        "moe_expert_gemm": (I32, [VP, I64, I64, VP, VP, VP, I32, I64, I64, VP, I64, VP, VP]),
+        "moe_expert_gemm_swiglu": (I32, [VP, I64, I64, VP, VP, VP, I32, I64, I64, VP, I64, VP, I64, VP, VP]),
+        "moe_expert_gemm_dgrad": (I32, [VP, I64, I64, VP, VP, VP, I32, I64, I64, VP, I64, VP, VP]),
+        "moe_expert_gemm_dgrad_swiglu": (I32, [VP, I64, I64, VP, VP, I64, VP, VP, I32, I64, I64, VP, I64, VP, VP]),
+        "moe_expert_gemm_wgrad": (I32, [VP, I64, VP, I64, I64, VP, VP, I32, I64, I64, VP, VP, VP]),
         "moe_adamw_create": (I32, [P(MoeAdamwTensor), I32, P(VP)]),
         "moe_adamw_destroy": (None, [VP]),
         "moe_adamw_launches": (I32, [VP]),
@@ -135,7 +140,8 @@ EXPORTED = ("moe_compact_all_tokens", "moe_choose_layout", "moe_ctx_create", "mo
             "moe_selftest_wait_timeout", "moe_sf_offset", "moe_strerror", "moe_plan_layout_noalloc",
             "moe_requant_weights_ue8m0", "moe_route", "moe_pack_mx_scales", "moe_route_workspace_size",
             "moe_router_prepare", "moe_sort_plan_workspace_size", "moe_sort_plan", "moe_sort_tokens",
-            "moe_unsort_tokens", "moe_unsort_tokens_backward", "moe_adamw_create", "moe_adamw_destroy",
+            "moe_unsort_tokens", "moe_unsort_tokens_backward", "moe_expert_gemm", "moe_expert_gemm_swiglu",
+            "moe_expert_gemm_dgrad", "moe_expert_gemm_dgrad_swiglu", "moe_expert_gemm_wgrad", "moe_adamw_create", "moe_adamw_destroy",
             "moe_adamw_launches", "moe_adamw_step")
 
 
@@ -513,6 +519,98 @@ def moe_unsort_tokens_backward(dout, y, src2dst, topk_weights, dy=None, dw=None,
                                            _ptr(topk_weights), T, topk, K, _elem("dout", dout), _ptr(dy), dy_ld,
                                            _ptr(dw), _stream(stream)), "moe_unsort_tokens_backward")
     return dy, dw
+
+
+def _expert_args(w, start, counts, status):
+    """Checks of the experts' products' common arguments: (E, N, C)."""
+    if w.dim() != 3:
+        raise ValueError("the weights must be [E, N, C]")
+    E, N, C = w.shape
+    _require_cuda("w", w, torch.bfloat16)
+    _require_cuda("start", start, torch.int32, E)
+    _require_cuda("counts", counts, torch.int32, E)
+    if not status.is_cuda or status.numel() * status.element_size() < 4:
+        raise ValueError("status must be a CUDA tensor of at least 4 bytes")
+    return E, N, C
+
+
+def _sorted_out(name, t, rows, cols, like, stream):
+    """An output of sorted rows, allocated when not given."""
+    if t is None:
+        t = _empty((rows, cols), torch.bfloat16, like, stream)
+    elif t.shape[0] != rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, expected {rows}")
+    return t, _rows(name, t, torch.bfloat16, cols)
+
+
+def moe_expert_gemm(x, w, start, counts, status, y=None, stream=None):
+    """Sorted rows x [rows, C], w [E, N, C] -> y [rows, N] = x W_e^T for each expert's rows; see include/moe.h.
+    status: CUDA tensor whose first int32 is the status word (a moe_sort_plan workspace, or 4 zeroed int32)."""
+    E, N, C = _expert_args(w, start, counts, status)
+    x_ld = _rows("x", x, torch.bfloat16, C)
+    y, y_ld = _sorted_out("y", y, x.shape[0], N, x, stream)
+    _check(_lib.moe_expert_gemm(_ptr(x), x_ld, x.shape[0], _ptr(w), _ptr(start), _ptr(counts), E, N, C, _ptr(y), y_ld,
+                                _ptr(status), _stream(stream)), "moe_expert_gemm")
+    return y
+
+
+def moe_expert_gemm_swiglu(x, w13, start, counts, status, h=None, gu=None, keep_gu=True, stream=None):
+    """Sorted rows x [rows, C], w13 [E, 2I, C] -> (h [rows, I], gu [rows, 2I]): the first product and its gated
+    activation.  keep_gu=False: gu (which only the gradient needs) is not stored, and None is returned for it."""
+    E, N, C = _expert_args(w13, start, counts, status)
+    if N % 2:
+        raise ValueError("w13 must have 2I rows per expert")
+    I = N // 2
+    x_ld = _rows("x", x, torch.bfloat16, C)
+    h, h_ld = _sorted_out("h", h, x.shape[0], I, x, stream)
+    gu_ld = 0
+    if keep_gu or gu is not None:
+        gu, gu_ld = _sorted_out("gu", gu, x.shape[0], N, x, stream)
+    _check(_lib.moe_expert_gemm_swiglu(_ptr(x), x_ld, x.shape[0], _ptr(w13), _ptr(start), _ptr(counts), E, I, C,
+                                       _ptr(gu), gu_ld, _ptr(h), h_ld, _ptr(status), _stream(stream)),
+           "moe_expert_gemm_swiglu")
+    return h, gu
+
+
+def moe_expert_gemm_dgrad(dy, w, start, counts, status, dx=None, stream=None):
+    """Gradient of moe_expert_gemm's rows: dy [rows, N], w [E, N, C] -> dx [rows, C]."""
+    E, N, C = _expert_args(w, start, counts, status)
+    dy_ld = _rows("dy", dy, torch.bfloat16, N)
+    dx, dx_ld = _sorted_out("dx", dx, dy.shape[0], C, dy, stream)
+    _check(_lib.moe_expert_gemm_dgrad(_ptr(dy), dy_ld, dy.shape[0], _ptr(w), _ptr(start), _ptr(counts), E, N, C,
+                                      _ptr(dx), dx_ld, _ptr(status), _stream(stream)), "moe_expert_gemm_dgrad")
+    return dx
+
+
+def moe_expert_gemm_dgrad_swiglu(dy, w2, gu, start, counts, status, dgu=None, stream=None):
+    """Gradient through the second product and the activation: dy [rows, N], w2 [E, N, I], gu [rows, 2I] as
+    moe_expert_gemm_swiglu stored it -> dgu [rows, 2I]."""
+    E, N, I = _expert_args(w2, start, counts, status)
+    dy_ld = _rows("dy", dy, torch.bfloat16, N)
+    gu_ld = _rows("gu", gu, torch.bfloat16, 2 * I)
+    if gu.shape[0] != dy.shape[0]:
+        raise ValueError(f"gu has {gu.shape[0]} rows, dy {dy.shape[0]}")
+    dgu, dgu_ld = _sorted_out("dgu", dgu, dy.shape[0], 2 * I, dy, stream)
+    _check(_lib.moe_expert_gemm_dgrad_swiglu(_ptr(dy), dy_ld, dy.shape[0], _ptr(w2), _ptr(gu), gu_ld, _ptr(start),
+                                             _ptr(counts), E, N, I, _ptr(dgu), dgu_ld, _ptr(status), _stream(stream)),
+           "moe_expert_gemm_dgrad_swiglu")
+    return dgu
+
+
+def moe_expert_gemm_wgrad(dy, x, start, counts, status, dw=None, stream=None):
+    """Gradient of the weights: dy [rows, N], x [rows, C] -> dw [E, N, C], zeros for experts without rows."""
+    E, N, C = counts.numel(), dy.shape[1], x.shape[1]
+    dy_ld, x_ld = _rows("dy", dy, torch.bfloat16), _rows("x", x, torch.bfloat16)
+    if x.shape[0] != dy.shape[0]:
+        raise ValueError(f"x has {x.shape[0]} rows, dy {dy.shape[0]}")
+    if dw is None:
+        dw = _empty((E, N, C), torch.bfloat16, dy, stream)
+    if tuple(dw.shape) != (E, N, C):
+        raise ValueError(f"dw is {tuple(dw.shape)}, expected {(E, N, C)}")
+    _expert_args(dw, start, counts, status)
+    _check(_lib.moe_expert_gemm_wgrad(_ptr(dy), dy_ld, _ptr(x), x_ld, x.shape[0], _ptr(start), _ptr(counts), E, N, C,
+                                      _ptr(dw), _ptr(status), _stream(stream)), "moe_expert_gemm_wgrad")
+    return dw
 
 
 class MoeAdamw:

@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "plan.cu", "quant.cu", "gemm.cu", "split_reduce.cu", "plan_noalloc.cu", "requant.cu",
-           "router.cu", "sort.cu", "adamw.cu"]
+           "router.cu", "sort.cu", "adamw.cu", "expert_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -325,6 +325,12 @@ moe::GemmArgs gemm_args(const moe_ctx* c, void* ws, int stage) {
 
 }  // namespace
 
+moe_status_t moe::encode_tiled_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int rank,
+                                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                                   CUtensorMapSwizzle swizzle) {
+  return make_map_nd(map, base, dt, rank, dims, strides, box, swizzle);
+}
+
 extern "C" {
 
 int64_t moe_compact_all_tokens(int64_t num_assignments, int32_t num_experts, int32_t block_e) {

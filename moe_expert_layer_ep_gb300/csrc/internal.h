@@ -7,6 +7,8 @@
 
 #include <utility>
 
+#include "../../include/moe.h"
+
 namespace moe {
 
 // Launch a layer kernel with programmatic dependent launch allowed (it may
@@ -206,6 +208,11 @@ inline bool router_folds(int64_t T, int64_t E, int sms) {
 cudaError_t launch_router_split(const float* w, uint16_t* planes, int64_t E, int64_t K, cudaStream_t s);
 cudaError_t launch_route(const CUtensorMap& map_x, const CUtensorMap& map_w, const RouterArgs& r, int grid, int topk,
                          float* logits, int32_t* ids, float* wts, cudaStream_t s);
+// A tiled tensor map of rank 2..5: dims[0] innermost (elements, contiguous),
+// strides[i] the byte stride of dims[i + 1].
+moe_status_t encode_tiled_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int rank,
+                              const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                              CUtensorMapSwizzle swizzle);
 cudaError_t launch_selftest_wait(int32_t* status, uint64_t timeout_ns, cudaStream_t s);
 
 
