@@ -409,6 +409,8 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
 /* One AdamW step over many tensors.  Per element, in fp32:
  *   g' = grad_scale * g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * where the root is taken of at least 2^-126, so that m = v = 0 is no step even
+ * for eps = 0.
  * param and grad are bf16 or fp32, rounded once when stored (to nearest: a
  * step smaller than half a bf16 spacing leaves a bf16 param as it was).
  * master (fp32, for a bf16 param, else NULL) is the value that is stepped;

@@ -24,6 +24,7 @@
 #include <string.h>
 
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "common.cuh"
@@ -33,11 +34,17 @@ namespace moe {
 
 namespace {
 
-constexpr int kAdamThreads = 256;
 constexpr int kStateBlock = 256;
 constexpr int kMaxTensors = 384;
-constexpr int64_t kChunkSmall = 2048;    // elements per CTA: one block per warp
-constexpr int64_t kChunkLarge = 8192;
+// Threads of a CTA and elements of its chunk: one block per warp where there is
+// little to do, else 16.  With 8-bit states,
+// 302 M bf16 elements with a 32-bit copy took 1039 us in CTAs of 256 threads and
+// 32768 elements, 817 us in 128 and 32768, 784 us in 64 and 32768, 737 us in 64
+// and 8192; with 32-bit states 151 M bf16 elements took 494 us in CTAs of 256
+// threads and 32768 elements, 501 us in 64 and 8192.
+__host__ __device__ constexpr int adam_threads(bool coded) { return coded ? 64 : 256; }
+__host__ __device__ constexpr int32_t chunk_small(bool coded) { return adam_threads(coded) / 32 * kStateBlock; }
+__host__ __device__ constexpr int32_t chunk_large(bool coded) { return chunk_small(coded) * 16; }
 
 struct AdamTable {
   void* p[kMaxTensors];
@@ -55,40 +62,65 @@ struct AdamTable {
 };
 
 struct AdamHyper {
-  float b1, omb1, b2, omb2, inv_root, eps, decay, step;
+  float b1, omb1, b2, omb2, inv_root, eps, decay, neg_step;
   const float* grad_scale;
 };
 
+// Four consecutive elements as loaded, zeros past n.
 template <typename T>
-__device__ __forceinline__ void load4(const void* base, int64_t i, int64_t n, bool whole, float (&f)[4]);
+struct Raw4;
 template <>
-__device__ __forceinline__ void load4<float>(const void* base, int64_t i, int64_t n, bool whole, float (&f)[4]) {
-  const float* b = static_cast<const float*>(base) + i;
-  if (whole) {
-    const float4 r = *reinterpret_cast<const float4*>(b);
-    f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = i + k < n ? b[k] : 0.0f;
+struct Raw4<float> {
+  float4 r;
+  __device__ __forceinline__ void load(const void* base, int32_t i, int32_t n, bool whole) {
+    const float* b = static_cast<const float*>(base) + i;
+    if (whole)
+      r = *reinterpret_cast<const float4*>(b);
+    else
+      r = make_float4(i < n ? b[0] : 0.0f, i + 1 < n ? b[1] : 0.0f, i + 2 < n ? b[2] : 0.0f, i + 3 < n ? b[3] : 0.0f);
   }
-}
+  __device__ __forceinline__ void open(float (&f)[4]) const { f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w; }
+};
 template <>
-__device__ __forceinline__ void load4<uint16_t>(const void* base, int64_t i, int64_t n, bool whole, float (&f)[4]) {
-  const uint16_t* b = static_cast<const uint16_t*>(base) + i;
-  if (whole) {
-    const uint2 r = *reinterpret_cast<const uint2*>(b);
+struct Raw4<uint16_t> {
+  uint2 r;
+  __device__ __forceinline__ void load(const void* base, int32_t i, int32_t n, bool whole) {
+    const uint16_t* b = static_cast<const uint16_t*>(base) + i;
+    if (whole) {
+      r = *reinterpret_cast<const uint2*>(b);
+    } else {
+      uint32_t e[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e[k] = i + k < n ? b[k] : 0u;
+      r = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+    }
+  }
+  __device__ __forceinline__ void open(float (&f)[4]) const {
     const float2 x = unpack_bf16x2(r.x), y = unpack_bf16x2(r.y);
     f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = i + k < n ? __uint_as_float(static_cast<uint32_t>(b[k]) << 16) : 0.0f;
   }
-}
+};
+// Four codes.
+template <>
+struct Raw4<uint8_t> {
+  uint32_t r;
+  __device__ __forceinline__ void load(const void* base, int32_t i, int32_t n, bool whole) {
+    const uint8_t* b = static_cast<const uint8_t*>(base) + i;
+    if (whole) {
+      r = *reinterpret_cast<const uint32_t*>(b);
+    } else {
+      r = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k < n) r |= static_cast<uint32_t>(b[k]) << (8 * k);
+    }
+  }
+};
 
 template <typename T>
-__device__ __forceinline__ void store4(void* base, int64_t i, int64_t n, bool whole, const float (&f)[4]);
+__device__ __forceinline__ void store4(void* base, int32_t i, int32_t n, bool whole, const float (&f)[4]);
 template <>
-__device__ __forceinline__ void store4<float>(void* base, int64_t i, int64_t n, bool whole, const float (&f)[4]) {
+__device__ __forceinline__ void store4<float>(void* base, int32_t i, int32_t n, bool whole, const float (&f)[4]) {
   float* b = static_cast<float*>(base) + i;
   if (whole) {
     *reinterpret_cast<float4*>(b) = make_float4(f[0], f[1], f[2], f[3]);
@@ -99,7 +131,7 @@ __device__ __forceinline__ void store4<float>(void* base, int64_t i, int64_t n, 
   }
 }
 template <>
-__device__ __forceinline__ void store4<uint16_t>(void* base, int64_t i, int64_t n, bool whole, const float (&f)[4]) {
+__device__ __forceinline__ void store4<uint16_t>(void* base, int32_t i, int32_t n, bool whole, const float (&f)[4]) {
   uint16_t* b = static_cast<uint16_t*>(base) + i;
   if (whole) {
     *reinterpret_cast<uint2*>(b) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
@@ -110,17 +142,7 @@ __device__ __forceinline__ void store4<uint16_t>(void* base, int64_t i, int64_t 
   }
 }
 
-// Four codes as one word, and back.
-__device__ __forceinline__ uint32_t load_codes(const void* base, int64_t i, int64_t n, bool whole) {
-  const uint8_t* b = static_cast<const uint8_t*>(base) + i;
-  if (whole) return *reinterpret_cast<const uint32_t*>(b);
-  uint32_t w = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (i + k < n) w |= static_cast<uint32_t>(b[k]) << (8 * k);
-  return w;
-}
-__device__ __forceinline__ void store_codes(void* base, int64_t i, int64_t n, bool whole, uint32_t w) {
+__device__ __forceinline__ void store_codes(void* base, int32_t i, int32_t n, bool whole, uint32_t w) {
   uint8_t* b = static_cast<uint8_t*>(base) + i;
   if (whole) {
     *reinterpret_cast<uint32_t*>(b) = w;
@@ -131,9 +153,8 @@ __device__ __forceinline__ void store_codes(void* base, int64_t i, int64_t n, bo
   }
 }
 
-// Largest of non-negative values over the warp.  As bit patterns, so that a
-// NaN (above every number there) is kept: the block's scale then is a NaN and
-// so are its states from there on, not silently zero.
+// Largest of non-negative values over the warp, as bit patterns (NaN is above
+// every number there).
 __device__ __forceinline__ float warp_max(float x) {
   return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
 }
@@ -142,11 +163,147 @@ __device__ __forceinline__ float warp_max(float x) {
 // number, so that its reciprocal is finite.
 __device__ __forceinline__ float block_scale(float top) { return top > 0.0f ? fmaxf(top, 1.17549435e-38f) : top; }
 
-// P, G: float or uint16_t (bf16).  Rounded operations are written one by one
-// (no contraction), so that codes next to a rounding boundary do not depend on
-// how the compiler fuses them.
+// Square root and reciprocal within 2 ulp: the correctly rounded forms cost
+// several times the instructions.  Subnormal arguments count as 0: the callers
+// keep them away where that matters.
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The larger, or NaN if either is one: a block with a NaN gets a NaN scale, and
+// its states are NaN from there on, not silently zero.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Byte k of a word of codes as a float less `bias`, without the conversion
+// unit: the byte becomes the low mantissa bits of 2^23.
+template <int kBias>
+__device__ __forceinline__ float byte_value(uint32_t w, int k) {
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u + k)) - static_cast<float>(8388608 + kBias);
+}
+constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
+// Low bytes of four words.  x + kMagic (|x| < 2^22) has the nearest integer to
+// x, ties to even, in its low mantissa bits, so these are codes modulo 256.
+__device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040u);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040u);
+  return __byte_perm(lo, hi, 0x5410u);
+}
+
+// One tensor's arrays, from a chunk's first element.
+struct Arrays {
+  char *p, *m, *v;
+  const char* g;
+  float *ms, *vs, *master;
+  int32_t n;   // elements of the tensor from there, as far as they matter to the chunk
+};
+
+// What a lane loads of the 256-element block at element b of the chunk: twice
+// four elements of each array.  kWhole: the block is complete and its arrays
+// are aligned, so all accesses are wide; else element by element.
+template <typename P, typename G, bool kMaster, bool kCoded, bool kWhole>
+struct Block {
+  Raw4<typename std::conditional<kMaster, float, P>::type> p[2];
+  Raw4<G> g[2];
+  Raw4<typename std::conditional<kCoded, uint8_t, float>::type> m[2], v[2];
+  float sm, sv;   // kCoded: the block's scales
+  __device__ __forceinline__ void load(const Arrays& t, int32_t b, int lane) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int32_t e = b + 128 * r + 4 * lane;
+      p[r].load(kMaster ? reinterpret_cast<const char*>(t.master) : t.p, e, t.n, kWhole);
+      g[r].load(t.g, e, t.n, kWhole);
+      m[r].load(t.m, e, t.n, kWhole);
+      v[r].load(t.v, e, t.n, kWhole);
+    }
+    if (kCoded) {
+      sm = t.ms[b / kStateBlock];
+      sv = t.vs[b / kStateBlock];
+    }
+  }
+  // The step on this block's values, and its stores.
+  __device__ __forceinline__ void step(const Arrays& t, const AdamHyper& h, float gs, int32_t b, int lane) const {
+    float top_m = 0.0f, top_v = 0.0f;
+    float fm[2][4], fv[2][4], root[2][4];   // root: sqrt(v), of at least the smallest normal number
+    const float dm = kCoded ? sm * (h.b1 / 16129.0f) : h.b1;   // (a code's step and the decay as one factor)
+    const float dv = kCoded ? sv * h.b2 : h.b2;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float fp[4], fg[4];
+      p[r].open(fp);
+      g[r].open(fg);
+      if constexpr (kCoded) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = byte_value<128>(m[r].r ^ 0x80808080u, k);
+          const float q = byte_value<0>(v[r].r, k) * (1.0f / 255.0f);
+          fm[r][k] = a * fabsf(a);
+          fv[r][k] = (q * q) * (q * q);
+        }
+      } else {
+        m[r].open(fm[r]);
+        v[r].open(fv[r]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = fg[k] * gs;
+        fm[r][k] = fmaf(fm[r][k], dm, x * h.omb1);
+        fv[r][k] = fmaf(fv[r][k], dv, x * x * h.omb2);
+        root[r][k] = sqrt_fast(fmaxf(fv[r][k], 1.17549435e-38f));
+        const float denom = fmaf(root[r][k], h.inv_root, h.eps);
+        fp[k] = fmaf(fm[r][k] * h.neg_step, rcp_fast(denom), fp[k] * h.decay);
+        if (kCoded) {
+          top_m = max_nan(top_m, fabsf(fm[r][k]));
+          top_v = max_nan(top_v, fv[r][k]);
+        }
+      }
+      const int32_t i = b + 128 * r + 4 * lane;
+      store4<P>(t.p, i, t.n, kWhole, fp);
+      if (kMaster) store4<float>(t.master, i, t.n, kWhole, fp);
+      if (!kCoded) {
+        store4<float>(t.m, i, t.n, kWhole, fm[r]);
+        store4<float>(t.v, i, t.n, kWhole, fv[r]);
+      }
+    }
+    if (kCoded) {
+      const float nm = block_scale(warp_max(top_m)), nv = block_scale(warp_max(top_v));
+      const float im = nm > 0.0f ? __fdiv_rn(1.0f, nm) : 0.0f;
+      const float iv = 65025.0f * __fsqrt_rn(nv > 0.0f ? __fdiv_rn(1.0f, nv) : 0.0f);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float qm[4], qv[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          qm[k] = fmaf(copysignf(sqrt_fast(fabsf(fm[r][k]) * im), fm[r][k]), 127.0f, kMagic);
+          // 255 (v / s)^(1/4), at least 1
+          const float q = fmaxf(sqrt_fast(root[r][k] * iv), 1.0f) + kMagic;
+          qv[k] = fv[r][k] > 0.0f ? q : 0.0f;
+        }
+        const int32_t i = b + 128 * r + 4 * lane;
+        store_codes(t.m, i, t.n, kWhole, low_bytes(qm[0], qm[1], qm[2], qm[3]));
+        store_codes(t.v, i, t.n, kWhole, low_bytes(qv[0], qv[1], qv[2], qv[3]));
+      }
+      if (lane == 0) {
+        t.ms[b / kStateBlock] = nm;
+        t.vs[b / kStateBlock] = nv;
+      }
+    }
+  }
+};
+
+// P, G: float or uint16_t (bf16).
 template <typename P, typename G, bool kMaster, bool kCoded>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable t, const AdamHyper h) {
+__global__ void __launch_bounds__(adam_threads(kCoded), kCoded ? 12 : 3)
+    adamw_kernel(const __grid_constant__ AdamTable t, const AdamHyper h) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t c = blockIdx.x;
   int lo = 0, hi = t.count - 1;   // first tensor whose chunks end after c
@@ -157,104 +314,46 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     else
       lo = mid + 1;
   }
-  const uint32_t first = lo ? t.chunk_end[lo - 1] : 0;
-  const int64_t n = t.n[lo];
-  const bool wide = t.wide[lo] != 0;
-  const int64_t begin = static_cast<int64_t>(c - first) * t.chunk;
-  const int64_t end = min(begin + t.chunk, n);
-  void* p = t.p[lo];
-  const void* g = t.g[lo];
-  void* m = t.m[lo];
-  void* v = t.v[lo];
-  float* master = t.master[lo];
+  const int64_t begin = static_cast<int64_t>(c - (lo ? t.chunk_end[lo - 1] : 0)) * t.chunk;
+  const int64_t left = t.n[lo] - begin;
+  Arrays a;
+  a.n = static_cast<int32_t>(left < t.chunk ? left : t.chunk);
+  a.p = static_cast<char*>(t.p[lo]) + begin * sizeof(P);
+  a.g = static_cast<const char*>(t.g[lo]) + begin * sizeof(G);
+  a.m = static_cast<char*>(t.m[lo]) + begin * (kCoded ? 1 : 4);
+  a.v = static_cast<char*>(t.v[lo]) + begin * (kCoded ? 1 : 4);
+  a.ms = kCoded ? t.ms[lo] + begin / kStateBlock : nullptr;
+  a.vs = kCoded ? t.vs[lo] + begin / kStateBlock : nullptr;
+  a.master = kMaster ? t.master[lo] + begin : nullptr;
+  // complete blocks by wide accesses, the rest (or all, of arrays that do not
+  // start on a boundary of four elements) element by element
+  const int32_t whole_end = t.wide[lo] ? a.n / kStateBlock * kStateBlock : 0;
+  constexpr int32_t kStep = chunk_small(kCoded);
+  int32_t b = warp * kStateBlock;
   pdl_wait();
   pdl_trigger();
   const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
-  for (int64_t b = begin + warp * kStateBlock; b < end; b += kAdamThreads / 32 * kStateBlock) {
-    const bool whole = wide && b + kStateBlock <= n;
-    float fp[2][4], fg[2][4], fm[2][4], fv[2][4];
-    uint32_t cm[2], cv[2];
-    float sm = 0.0f, sv = 0.0f;
-    if (kCoded) {
-      sm = t.ms[lo][b / kStateBlock];
-      sv = t.vs[lo][b / kStateBlock];
+  if (kCoded) {
+    // states in 8 bits take enough arithmetic that the next block has to be on
+    // its way meanwhile; in 32 bits, more warps serve better
+    Block<P, G, kMaster, kCoded, true> cur, next;
+    if (b < whole_end) cur.load(a, b, lane);
+    for (; b < whole_end; b += kStep) {
+      if (b + kStep < whole_end) next.load(a, b + kStep, lane);
+      cur.step(a, h, gs, b, lane);
+      cur = next;
     }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t i = b + 128 * r + 4 * lane;
-      if (kMaster)
-        load4<float>(master, i, n, whole, fp[r]);
-      else
-        load4<P>(p, i, n, whole, fp[r]);
-      load4<G>(g, i, n, whole, fg[r]);
-      if (kCoded) {
-        cm[r] = load_codes(m, i, n, whole);
-        cv[r] = load_codes(v, i, n, whole);
-      } else {
-        load4<float>(m, i, n, whole, fm[r]);
-        load4<float>(v, i, n, whole, fv[r]);
-      }
+  } else {
+    for (; b < whole_end; b += kStep) {
+      Block<P, G, kMaster, kCoded, true> cur;
+      cur.load(a, b, lane);
+      cur.step(a, h, gs, b, lane);
     }
-    float top_m = 0.0f, top_v = 0.0f;
-    float root[2][4];   // sqrt(v)
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (kCoded) {
-          const float a = __fmul_rn(static_cast<float>(static_cast<int8_t>(cm[r] >> (8 * k))), 1.0f / 127.0f);
-          fm[r][k] = __fmul_rn(__fmul_rn(a, fabsf(a)), sm);
-          float q = __fmul_rn(static_cast<float>((cv[r] >> (8 * k)) & 0xFFu), 1.0f / 255.0f);
-          q = __fmul_rn(q, q);
-          fv[r][k] = __fmul_rn(__fmul_rn(q, q), sv);
-        }
-        const float x = __fmul_rn(fg[r][k], gs);
-        fm[r][k] = __fadd_rn(__fmul_rn(fm[r][k], h.b1), __fmul_rn(x, h.omb1));
-        fv[r][k] = __fadd_rn(__fmul_rn(fv[r][k], h.b2), __fmul_rn(__fmul_rn(x, x), h.omb2));
-        root[r][k] = __fsqrt_rn(fv[r][k]);
-        const float denom = __fadd_rn(__fmul_rn(root[r][k], h.inv_root), h.eps);
-        fp[r][k] = __fsub_rn(__fmul_rn(fp[r][k], h.decay), __fmul_rn(__fdiv_rn(fm[r][k], denom), h.step));
-        if (kCoded) {
-          top_m = __uint_as_float(max(__float_as_uint(top_m), __float_as_uint(fabsf(fm[r][k]))));
-          top_v = __uint_as_float(max(__float_as_uint(top_v), __float_as_uint(fabsf(fv[r][k]))));
-        }
-      }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t i = b + 128 * r + 4 * lane;
-      store4<P>(p, i, n, whole, fp[r]);
-      if (kMaster) store4<float>(master, i, n, whole, fp[r]);
-      if (!kCoded) {
-        store4<float>(m, i, n, whole, fm[r]);
-        store4<float>(v, i, n, whole, fv[r]);
-      }
-    }
-    if (kCoded) {
-      const float nm = block_scale(warp_max(top_m)), nv = block_scale(warp_max(top_v));
-      const float im = nm > 0.0f ? __fdiv_rn(1.0f, nm) : 0.0f;
-      const float iv = __fsqrt_rn(nv > 0.0f ? __fdiv_rn(1.0f, nv) : 0.0f);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t wm = 0, wv = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          int qm = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(fm[r][k]), im)), 127.0f));
-          qm = min(qm, 127);
-          if (fm[r][k] < 0.0f) qm = -qm;
-          int qv = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(root[r][k], iv)), 255.0f));
-          qv = min(max(qv, fv[r][k] > 0.0f ? 1 : 0), 255);
-          wm |= static_cast<uint32_t>(qm & 0xFF) << (8 * k);
-          wv |= static_cast<uint32_t>(qv) << (8 * k);
-        }
-        const int64_t i = b + 128 * r + 4 * lane;
-        store_codes(m, i, n, whole, wm);
-        store_codes(v, i, n, whole, wv);
-      }
-      if (lane == 0) {
-        t.ms[lo][b / kStateBlock] = nm;
-        t.vs[lo][b / kStateBlock] = nv;
-      }
-    }
+  }
+  for (; b < a.n; b += kStep) {
+    Block<P, G, kMaster, kCoded, false> cur;
+    cur.load(a, b, lane);
+    cur.step(a, h, gs, b, lane);
   }
 }
 
@@ -324,7 +423,7 @@ void add_launch(moe_adamw* a, int kind, const std::vector<const moe_adamw_tensor
   memset(&l.table, 0, sizeof(l.table));
   l.kind = kind;
   l.table.count = static_cast<int32_t>(ts.size());
-  l.table.chunk = static_cast<int32_t>(total > (int64_t(1) << 23) ? moe::kChunkLarge : moe::kChunkSmall);
+  l.table.chunk = total > (int64_t(1) << 23) ? moe::chunk_large(kind & 8) : moe::chunk_small(kind & 8);
   uint32_t end = 0;
   for (size_t i = 0; i < ts.size(); ++i) {
     const moe_adamw_tensor_t& t = *ts[i];
@@ -408,10 +507,10 @@ moe_status_t moe_adamw_step(const moe_adamw* opt, const moe_adamw_hyper_t* h, co
   a.inv_root = static_cast<float>(1.0 / sqrt(1.0 - pow(h->beta2, t)));
   a.eps = static_cast<float>(h->eps);
   a.decay = static_cast<float>(1.0 - h->lr * h->weight_decay);
-  a.step = static_cast<float>(h->lr / (1.0 - pow(h->beta1, t)));
+  a.neg_step = static_cast<float>(-h->lr / (1.0 - pow(h->beta1, t)));
   a.grad_scale = grad_scale;
   for (const moe_adamw::Launch& l : opt->launches) {
-    const cudaError_t e = moe::launch_pdl(moe::adam_kernel(l.kind), dim3(l.chunks), dim3(moe::kAdamThreads), 0,
+    const cudaError_t e = moe::launch_pdl(moe::adam_kernel(l.kind), dim3(l.chunks), dim3(moe::adam_threads(l.kind & 8)), 0,
                                           static_cast<cudaStream_t>(stream), l.table, a);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
