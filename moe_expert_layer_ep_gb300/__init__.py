@@ -151,20 +151,21 @@ def _check(code, what):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if stream is None:   # the current stream's handle, without a torch.cuda.Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _require_cuda(name, t, dtype=None, numel=None):
+    if (t.is_cuda and (dtype is None or t.dtype is dtype) and (numel is None or t.numel() == numel)
+            and t.is_contiguous()):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -411,16 +412,21 @@ def _rows(name, t, dtype=None, cols=None):
     """A matrix of rows that are contiguous in themselves; returns its row stride."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be a matrix with contiguous rows")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
-    ld = t.stride(0)
-    if t.shape[0] > 1 and ld < t.shape[1]:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    n, c = t.shape
+    if cols is not None and c != cols:
+        raise ValueError(f"{name} has {c} columns, expected {cols}")
+    if t.is_contiguous():
+        return c
+    ld, one = t.stride()
+    if one != 1 and c > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if n > 1 and ld < c:
         raise ValueError(f"{name}'s rows overlap")
-    return ld if ld > t.shape[1] else t.shape[1]
+    return ld if ld > c else c
 
 
 def _elem(name, t):
@@ -444,16 +450,20 @@ def moe_sort_plan(topk_ids, E_global, E_local=None, expert_start=0, src2dst=None
     _require_cuda("topk_ids", topk_ids, torch.int32)
     if src2dst is None:
         src2dst = _empty((T, topk), torch.int32, topk_ids, stream)
+    else:
+        _require_cuda("src2dst", src2dst, torch.int32, T * topk)
     if start is None:
         start = _empty((E_local,), torch.int32, topk_ids, stream)
+    else:
+        _require_cuda("start", start, torch.int32, E_local)
     if counts is None:
         counts = _empty((E_local,), torch.int32, topk_ids, stream)
+    else:
+        _require_cuda("counts", counts, torch.int32, E_local)
     if ws is None:
         ws = _empty((max(16, moe_sort_plan_workspace_size(T, topk, E_local)),), torch.uint8, topk_ids, stream)
-    _require_cuda("src2dst", src2dst, torch.int32, T * topk)
-    _require_cuda("start", start, torch.int32, E_local)
-    _require_cuda("counts", counts, torch.int32, E_local)
-    _require_cuda("ws", ws, torch.uint8)
+    else:
+        _require_cuda("ws", ws, torch.uint8)
     _check(_lib.moe_sort_plan(_ptr(topk_ids), T, topk, E_global, E_local, expert_start, _ptr(src2dst), _ptr(start),
                               _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)), "moe_sort_plan")
     return src2dst, start, counts

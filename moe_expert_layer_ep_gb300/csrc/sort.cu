@@ -25,7 +25,7 @@ namespace moe {
 namespace {
 
 constexpr int kSortThreads = 256;
-constexpr int kSortBatch = 4;     // row segments a thread has in flight
+constexpr int kSortBatch = 4;     // row segments a thread has in flight (sort; element-wide unsort)
 constexpr int kJBatch = 8;        // selections handled together
 
 struct SortArgs {
@@ -75,12 +75,20 @@ struct Pack<float, 1> {
   __device__ static Raw close(const float (&f)[1]) { return f[0]; }
 };
 
-// Destination row of selection j of token t, -1 when there is none (dropped,
-// or outside the sorted buffer).
-__device__ __forceinline__ int64_t dest(const SortArgs& a, int64_t t, int j) {
-  if (j >= a.topk) return -1;
-  const int64_t d = a.src2dst[t * a.topk + j];
-  return d < a.rows ? d : -1;
+// Each token's destination rows (-1: dropped, or outside the sorted buffer) and
+// weights, read once into shared memory by the token's threads.
+struct Picks {
+  int32_t d[kSortThreads / 32][kMaxTopk];
+  float w[kSortThreads / 32][kMaxTopk];
+};
+__device__ __forceinline__ void load_picks(const SortArgs& a, Picks& s, int64_t t, int slot, int lane, int lanes) {
+  if (t < a.T)
+    for (int j = lane; j < a.topk; j += lanes) {
+      const int32_t d = a.src2dst[t * a.topk + j];
+      s.d[slot][j] = d < a.rows ? d : -1;
+      s.w[slot][j] = a.w ? a.w[t * a.topk + j] : 1.0f;
+    }
+  __syncthreads();
 }
 
 template <typename E, int kVec>
@@ -90,19 +98,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(SortArgs a) {
   const int lanes = 1 << a.lanes_log2;
   const int lane = threadIdx.x & (lanes - 1);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+  __shared__ Picks s;
+  const int slot = threadIdx.x >> a.lanes_log2;
   pdl_wait();
   pdl_trigger();
+  load_picks(a, s, t, slot, lane, lanes);
   if (t >= a.T) return;
   const E* xrow = static_cast<const E*>(a.x) + t * a.x_ld;
   E* out = static_cast<E*>(a.out);
   const int64_t step = static_cast<int64_t>(lanes) * kVec;
-  for (int64_t c0 = static_cast<int64_t>(lane) * kVec; c0 < a.K; c0 += kSortBatch * step) {
+  const int64_t first = static_cast<int64_t>(lane) * kVec + blockIdx.y * kSortBatch * step;
+  for (int64_t c0 = first; c0 < a.K; c0 += gridDim.y * kSortBatch * step) {
     Raw v[kSortBatch];
 #pragma unroll
     for (int b = 0; b < kSortBatch; ++b)
       if (c0 + b * step < a.K) v[b] = *reinterpret_cast<const Raw*>(xrow + c0 + b * step);
     for (int j = 0; j < a.topk; ++j) {
-      const int64_t d = dest(a, t, j);
+      const int32_t d = s.d[slot][j];
       if (d < 0) continue;
       E* orow = out + d * a.out_ld + c0;
 #pragma unroll
@@ -112,41 +124,60 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(SortArgs a) {
   }
 }
 
-template <typename E, int kVec>
+// kJ selections of kSeg row segments per thread at once: eight loads in flight
+// whatever topk is.
+template <typename E, int kVec, int kJ>
 __global__ void __launch_bounds__(kSortThreads) unsort_tokens_kernel(SortArgs a) {
   using P = Pack<E, kVec>;
   using Raw = typename P::Raw;
+  constexpr int kSeg = (kVec == 1 ? 16 : 8) / kJ;
+  __shared__ Picks s;
   const int lanes = 1 << a.lanes_log2;
-  const int lane = threadIdx.x & (lanes - 1);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+  const int lane = threadIdx.x & (lanes - 1), slot = threadIdx.x >> a.lanes_log2;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + slot;
   pdl_wait();
   pdl_trigger();
+  load_picks(a, s, t, slot, lane, lanes);
   if (t >= a.T) return;
   const E* y = static_cast<const E*>(a.x);
   E* orow = static_cast<E*>(a.out) + t * a.out_ld;
-  for (int64_t c = static_cast<int64_t>(lane) * kVec; c < a.K; c += static_cast<int64_t>(lanes) * kVec) {
-    float acc[kVec];
+  const int64_t step = static_cast<int64_t>(lanes) * kVec;
+  const int64_t first = static_cast<int64_t>(lane) * kVec + blockIdx.y * kSeg * step;
+  for (int64_t c = first; c < a.K; c += gridDim.y * kSeg * step) {
+    float acc[kSeg][kVec];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < a.topk; j0 += kJBatch) {
-      Raw v[kJBatch];
-      int64_t d[kJBatch];
+    for (int g = 0; g < kSeg; ++g)
 #pragma unroll
-      for (int jj = 0; jj < kJBatch; ++jj) {
-        d[jj] = dest(a, t, j0 + jj);
-        if (d[jj] >= 0) v[jj] = *reinterpret_cast<const Raw*>(y + d[jj] * a.x_ld + c);
+      for (int i = 0; i < kVec; ++i) acc[g][i] = 0.0f;
+    for (int j0 = 0; j0 < a.topk; j0 += kJ) {
+      Raw v[kSeg][kJ];
+      // every load of the batch before the first use
+#pragma unroll
+      for (int jj = 0; jj < kJ; ++jj) {
+        const int j = j0 + jj;
+        const bool on = j < a.topk && s.d[slot][j] >= 0;
+        const E* row = y + (on ? s.d[slot][j] : 0) * a.x_ld + c;
+#pragma unroll
+        for (int g = 0; g < kSeg; ++g)
+          if (on && c + g * step < a.K) v[g][jj] = *reinterpret_cast<const Raw*>(row + g * step);
       }
 #pragma unroll
-      for (int jj = 0; jj < kJBatch; ++jj) {
-        if (d[jj] < 0) continue;
-        const float w = a.w ? a.w[t * a.topk + j0 + jj] : 1.0f;
-        float f[kVec];
-        P::open(v[jj], f);
+      for (int jj = 0; jj < kJ; ++jj) {
+        const int j = j0 + jj;
+        if (j >= a.topk || s.d[slot][j] < 0) continue;
+        const float w = s.w[slot][j];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+        for (int g = 0; g < kSeg; ++g) {
+          float f[kVec];
+          P::open(v[g][jj], f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[g][i] = fmaf(w, f[i], acc[g][i]);
+        }
       }
     }
-    *reinterpret_cast<Raw*>(orow + c) = P::close(acc);
+#pragma unroll
+    for (int g = 0; g < kSeg; ++g)
+      if (c + g * step < a.K) *reinterpret_cast<Raw*>(orow + c + g * step) = P::close(acc[g]);
   }
 }
 
@@ -154,47 +185,61 @@ template <typename E, int kVec>
 __global__ void __launch_bounds__(kSortThreads) unsort_backward_kernel(SortArgs a) {
   using P = Pack<E, kVec>;
   using Raw = typename P::Raw;
+  constexpr int kSeg = kVec == 1 ? 2 : 1;
   __shared__ float s_dot[kSortThreads / 32][kJBatch];
   const int lanes = 1 << a.lanes_log2;
-  const int lane = threadIdx.x & (lanes - 1), warp = threadIdx.x >> 5;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+  const int lane = threadIdx.x & (lanes - 1), warp = threadIdx.x >> 5, slot = threadIdx.x >> a.lanes_log2;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + slot;
+  __shared__ Picks s;
   pdl_wait();
   pdl_trigger();
+  load_picks(a, s, t, slot, lane, lanes);
   const bool live = t < a.T;
   const E* drow = static_cast<const E*>(a.x) + t * a.x_ld;
   const E* y = static_cast<const E*>(a.y);
   E* dy = static_cast<E*>(a.out);
+  const int64_t step = static_cast<int64_t>(lanes) * kVec;
   for (int j0 = 0; j0 < a.topk; j0 += kJBatch) {
-    int64_t d[kJBatch];
+    int32_t d[kJBatch];
     float w[kJBatch], dot[kJBatch];
 #pragma unroll
     for (int jj = 0; jj < kJBatch; ++jj) {
-      d[jj] = live ? dest(a, t, j0 + jj) : -1;
-      w[jj] = d[jj] >= 0 ? a.w[t * a.topk + j0 + jj] : 0.0f;
+      const bool on = live && j0 + jj < a.topk;
+      d[jj] = on ? s.d[slot][j0 + jj] : -1;
+      w[jj] = on ? s.w[slot][j0 + jj] : 0.0f;
       dot[jj] = 0.0f;
     }
-    for (int64_t c = static_cast<int64_t>(lane) * kVec; live && c < a.K; c += static_cast<int64_t>(lanes) * kVec) {
-      const Raw rd = *reinterpret_cast<const Raw*>(drow + c);
-      Raw v[kJBatch];
+    for (int64_t c = static_cast<int64_t>(lane) * kVec; live && c < a.K; c += kSeg * step) {
+      Raw rd[kSeg], v[kSeg][kJBatch];
+#pragma unroll
+      for (int i = 0; i < kSeg; ++i)
+        if (c + i * step < a.K) rd[i] = *reinterpret_cast<const Raw*>(drow + c + i * step);
       if (y) {
 #pragma unroll
         for (int jj = 0; jj < kJBatch; ++jj)
-          if (d[jj] >= 0) v[jj] = *reinterpret_cast<const Raw*>(y + d[jj] * a.y_ld + c);
+#pragma unroll
+          for (int i = 0; i < kSeg; ++i)
+            if (d[jj] >= 0 && c + i * step < a.K)
+              v[i][jj] = *reinterpret_cast<const Raw*>(y + d[jj] * a.y_ld + c + i * step);
       }
-      float g[kVec];
-      P::open(rd, g);
 #pragma unroll
-      for (int jj = 0; jj < kJBatch; ++jj) {
-        if (d[jj] < 0) continue;
-        float f[kVec];
-        if (y) {
-          P::open(v[jj], f);
+      for (int i = 0; i < kSeg; ++i) {
+        if (c + i * step >= a.K) continue;
+        float g[kVec];
+        P::open(rd[i], g);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) dot[jj] = fmaf(g[i], f[i], dot[jj]);
+        for (int jj = 0; jj < kJBatch; ++jj) {
+          if (d[jj] < 0) continue;
+          float f[kVec];
+          if (y) {
+            P::open(v[i][jj], f);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) dot[jj] = fmaf(g[e], f[e], dot[jj]);
+          }
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) f[e] = w[jj] * g[e];
+          *reinterpret_cast<Raw*>(dy + d[jj] * a.out_ld + c + i * step) = P::close(f);
         }
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) f[i] = w[jj] * g[i];
-        *reinterpret_cast<Raw*>(dy + d[jj] * a.out_ld + c) = P::close(f);
       }
     }
     if (!y) continue;
@@ -221,9 +266,12 @@ using SortKernel = void (*)(SortArgs);
 enum SortOp { kOpSort, kOpUnsort, kOpBackward };
 
 template <typename E, int kVec>
-SortKernel kernel_of(SortOp op) {
+SortKernel kernel_of(SortOp op, int topk) {
   if (op == kOpSort) return sort_tokens_kernel<E, kVec>;
-  return op == kOpUnsort ? unsort_tokens_kernel<E, kVec> : unsort_backward_kernel<E, kVec>;
+  if (op == kOpBackward) return unsort_backward_kernel<E, kVec>;
+  if (topk == 1) return unsort_tokens_kernel<E, kVec, 1>;
+  if (topk == 2) return unsort_tokens_kernel<E, kVec, 2>;
+  return topk <= 4 ? unsort_tokens_kernel<E, kVec, 4> : unsort_tokens_kernel<E, kVec, 8>;
 }
 
 // Row accesses are 16 bytes wide when every row starts on a 16-byte boundary
@@ -237,17 +285,29 @@ moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
   const bool vec = bases % 16 == 0 && a.K % wide == 0 && a.x_ld % wide == 0 && a.out_ld % wide == 0 &&
                    (!has_y || a.y_ld % wide == 0);
   const int64_t units = vec ? a.K / wide : a.K;
+  // segments a thread has in flight, and the threads that cover a row with them
+  int64_t seg = kSortBatch;
+  if (op == kOpUnsort) seg = (vec ? 8 : 16) / (a.topk == 1 ? 1 : a.topk == 2 ? 2 : a.topk <= 4 ? 4 : 8);
+  if (op == kOpBackward) seg = vec ? 1 : 2;
   a.lanes_log2 = 5;
-  while (a.lanes_log2 < 8 && (int64_t(1) << a.lanes_log2) < units) ++a.lanes_log2;
+  while (a.lanes_log2 < 8 && (seg << a.lanes_log2) < units) ++a.lanes_log2;
   const int64_t per_cta = kSortThreads >> a.lanes_log2;
   const int64_t grid = (a.T + per_cta - 1) / per_cta;
+  // few tokens: their columns are spread over CTAs too (not in the backward
+  // kernel, whose dot products run over a token's whole row)
+  int64_t parts = (units + (seg << a.lanes_log2) - 1) / (seg << a.lanes_log2);
+  const int64_t room = 1024 / grid;
+  if (parts > room) parts = room;
+  if (op == kOpBackward || parts < 1) parts = 1;
   SortKernel k;
   if (elem == MOE_ELEM_F32)
-    k = vec ? kernel_of<float, 4>(op) : kernel_of<float, 1>(op);
+    k = vec ? kernel_of<float, 4>(op, a.topk) : kernel_of<float, 1>(op, a.topk);
   else
-    k = vec ? kernel_of<uint16_t, 8>(op) : kernel_of<uint16_t, 1>(op);
-  return launch_pdl(k, dim3(static_cast<unsigned>(grid)), dim3(kSortThreads), 0, s, a) == cudaSuccess ? MOE_OK
-                                                                                                 : MOE_ERR_CUDA;
+    k = vec ? kernel_of<uint16_t, 8>(op, a.topk) : kernel_of<uint16_t, 1>(op, a.topk);
+  return launch_pdl(k, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(parts)), dim3(kSortThreads), 0, s, a) ==
+                 cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
