@@ -10,27 +10,39 @@
 //                 dg = dh u s (1 + g (1 - s)),  du = dh g s
 //   kWgrad        dW_e  = sum over r of dy[r]^T x[r]      (0 without rows)
 //
-// All are 128 x 256 output tiles summed over 64-element blocks of the
-// reduction, and differ in which operand's reduction runs along memory rows:
-//   kFwd    A = x (K-major)        B = W (K-major)
-//   kDgrad  A = dy (K-major)       B = W (MN-major: the output column runs along W's rows)
-//   kWgrad  A = dy (MN-major)      B = x (MN-major), reduction over the expert's rows
-// A K-major tile is one box of 64 elements x rows; an MN-major tile is one
-// 64 x 64 box per 64 output rows / columns, so no operand is ever transposed
-// in memory.  Everything is read where the forward pass left it.
+// Two kernels.
 //
-// An expert's rows are any consecutive rows (start, counts), 128 of them per
-// row block.  Rows of a block beyond the expert's are multiplied like the
-// others (they only make output rows that are not stored); in kWgrad, where
-// rows are summed over, the last reduction block's rows beyond the expert's are
+// Rows (all but kWgrad).  The sorted rows are few and uneven, the weights' rows
+// many and even, so the weights are the M side of the MMA and the tokens its N
+// side: D = W X^T, a tile of 256 features x n tokens.  An expert's rows are cut
+// into as few blocks of at most 256 as will do, equally tall up to a multiple
+// of 32, so uneven experts cost the MMAs of at most 31 rows too many, not of
+// half a 128-row block each (which took a sixth to a quarter more at 512 and
+// 256 rows per expert).  A tile is worked on by a CTA pair: M = 256 over the
+// two, each CTA staging its own 128 weight rows and half of the tokens.  Per
+// 64-element block of the reduction that is 32 KB per SM instead of the 48 KB
+// of a 128 x 256 tile on one SM, whose writes and reads of shared memory (96 KB
+// at about 138 B per clock) took 700 cycles for 512 cycles of MMA.
+//   kFwd    A = W rows (K-major)                  B = x rows (K-major)
+//   kDgrad  A = W columns (MN-major: the feature  B = dy rows (K-major)
+//           runs along W's memory rows)
+// The accumulator holds features in lanes and tokens in columns; the epilogue
+// turns it around in registers (lanes exchange with their neighbours, two
+// values a shuffle) and in 32-token store tiles, so memory sees whole rows.
+// kFwdSwiglu's CTA holds 64 gate rows and the 64 up rows of the same features;
+// the warps of a feature's g and of its u hand each other half of a chunk's
+// tokens and form h of the other half.
+//
+// Weights' gradient (kWgrad).  dW = dy^T x, a tile of 128 x 256 on one CTA, both
+// operands MN-major (64 x 64 boxes, no transposed copies), summed over the
+// expert's rows 64 at a time.  Rows beyond the expert's in the last block are
 // cleared in shared memory before the product, so whatever lies there, NaN
-// included, does not count.
+// included, does not count.  (In the other products such rows only make output
+// rows that are not stored.)
 //
-// One persistent CTA per SM: warp 0 TMA producer, warp 1 MMA issue, warps 2-5
-// epilogue (one per 32 accumulator rows), four stages of 48 KB, two
+// Both: one persistent CTA per SM: warp 0 TMA producer, warp 1 MMA issue, warps
+// 2-5 epilogue (one per 32 accumulator lanes, independent of one another), two
 // accumulators so that a tile's epilogue runs beside the next tile's MMAs.
-// The epilogue warps are independent: a warp whose 32 rows all exist stores
-// through its own shared-memory tiles and TMA, others row by row.
 #include <string.h>
 
 #include <initializer_list>
@@ -44,35 +56,45 @@ namespace {
 
 enum ExpertOp { kFwd, kFwdSwiglu, kDgrad, kDgradSwiglu, kWgrad };
 
-constexpr int kStages = 4;
-constexpr int kTileM = 128;
-constexpr int kTileN = 256;
 constexpr int kBlockK = 64;                          // elements: 128 bytes, one swizzle atom
-constexpr int kABytes = kTileM * kBlockK * 2;        // 16 KB
-constexpr int kBBytes = kTileN * kBlockK * 2;        // 32 KB
 constexpr int kBoxBytes = 64 * kBlockK * 2;          // an MN-major box: 64 x 64 elements
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kStgTile = 32 * 64;                    // a store tile: 32 rows x 32 columns
-constexpr int kStgPerWarp = 3;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kXchg = 3 * 1024;                      // kFwdSwiglu: a warp's tile and a half, and from there twice 16
+                                                     // tokens x 32 lanes in fp32
+constexpr int kMaxStages = 6, kMaxEpiWarps = 8;
 
-constexpr int kOffA = 0;
-constexpr int kOffB = kOffA + kStages * kABytes;
-constexpr int kOffStg = kOffB + kStages * kBBytes;
-constexpr int kOffBar = kOffStg + kEpiWarps * kStgPerWarp * kStgTile;
-constexpr int kNumBars = 2 * kStages + 5;            // full, empty; tfull[2], tempty[2]; done
-constexpr int kOffHolder = kOffBar + kNumBars * 8;
-constexpr int kOffAbort = kOffHolder + 4;
-constexpr int kOffScan = kOffAbort + 4;              // warps' sums of the block scan
-constexpr int kOffCum = kOffScan + 64;               // row blocks of the experts before e, [E + 1]
-constexpr int kSmemBytes = kOffCum + 4 * (kMaxLocalExperts + 1) + 1024;   // + alignment slack
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+// Shared memory: the stages, the epilogue warps' tiles, then the same for all.
+constexpr int kNumBars = 2 * kMaxStages + 9;         // full, empty; tfull[2], tempty[2]; done; xchg[4]
+constexpr int kTailHolder = kNumBars * 8;
+constexpr int kTailAbort = kTailHolder + 4;
+constexpr int kTailScan = kTailAbort + 4;            // warps' sums of the block scan
+constexpr int kTailCum = kTailScan + 64;             // token blocks of the experts before e, [E + 1]
+constexpr int kTailBytes = kTailCum + 4 * (kMaxLocalExperts + 1) + 1024;   // + alignment slack
 
-constexpr uint32_t kIdesc = (1u << 4)       // D fp32
-                            | (1u << 7)     // A bf16
-                            | (1u << 10)    // B bf16
-                            | (static_cast<uint32_t>(kTileN >> 3) << 17) | (static_cast<uint32_t>(kTileM >> 4) << 24);
+// Stages, epilogue warps and their shared memory, by operator.  The activation
+// and its gradient take the epilogue more arithmetic and more bytes than the
+// product alone, so they get eight warps, two per 32 lanes, for a stage less.
+template <ExpertOp kOp>
+struct Cfg {
+  static constexpr bool kAct = kOp == kFwdSwiglu || kOp == kDgradSwiglu;
+  static constexpr int kStages = kOp == kWgrad ? 4 : kAct ? 5 : 6;
+  static constexpr int kStage = kOp == kWgrad ? 48 * 1024 : 32 * 1024;
+  static constexpr int kEpiWarps = kAct ? 8 : 4;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kTiles = 3;                       // store tiles of an epilogue warp
+  static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 4 * 1024 : kTiles * kStgTile;
+  static constexpr int kOffStg = kStages * kStage;
+  static constexpr int kOffTail = kOffStg + kEpiWarps * kStgBytes;
+  static constexpr int kSmem = kOffTail + kTailBytes;
+  static_assert(kSmem <= 227 * 1024 && kStages <= kMaxStages && kEpiWarps <= kMaxEpiWarps, "shared memory");
+};
+
+// D fp32, A and B bf16; M and N are added
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10);
+__host__ __device__ constexpr uint32_t idesc_mn(int m, int n) {
+  return (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
 constexpr uint32_t kAMnMajor = 1u << 15, kBMnMajor = 1u << 16;
 
 struct ExpertArgs {
@@ -80,7 +102,7 @@ struct ExpertArgs {
   const int32_t* counts;    // [E] rows
   int32_t E;
   int64_t rows;             // rows of the sorted buffers
-  int32_t n_tiles;          // output column tiles
+  int32_t n_tiles;          // output column (feature) tiles
   int32_t m_tiles;          // kWgrad: output row tiles per expert
   int32_t k_blocks;         // reduction blocks (not kWgrad)
   int64_t n_rows;           // kWgrad: output rows of an expert (N)
@@ -95,58 +117,17 @@ struct ExpertArgs {
   uint64_t timeout_ns;
 };
 
-// One output tile.
-struct Tile {
-  int expert;
-  int64_t row0;   // first sorted row: of the block, or (kWgrad) of the expert
-  int valid;      // rows of the block that carry a token
-  int mt;         // kWgrad: output row tile
-  int nt;         // output column tile
-  int kb;         // reduction blocks
-  int tail;       // kWgrad: rows of the last reduction block
-};
-
 // An expert's rows, none where its numbers do not fit the buffer.
 __device__ __forceinline__ int expert_rows(const ExpertArgs& g, int e) {
   const int64_t n = g.counts[e], s = g.start[e];
   return n > 0 && s >= 0 && s + n <= g.rows ? static_cast<int>(n) : 0;
 }
 
-template <ExpertOp kOp>
-__device__ __forceinline__ Tile tile_at(const ExpertArgs& g, const int32_t* s_cum, int64_t t) {
-  Tile r;
-  if constexpr (kOp == kWgrad) {
-    const int64_t per = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
-    r.expert = static_cast<int>(t / per);
-    const int64_t i = t - r.expert * per;
-    r.mt = static_cast<int>(i / g.n_tiles);
-    r.nt = static_cast<int>(i - static_cast<int64_t>(r.mt) * g.n_tiles);
-    const int n = expert_rows(g, r.expert);
-    r.row0 = g.start[r.expert];
-    r.valid = kTileM;
-    r.kb = (n + kBlockK - 1) / kBlockK;
-    r.tail = n - (r.kb - 1) * kBlockK;
-  } else {
-    const int64_t b = t / g.n_tiles;
-    r.nt = static_cast<int>(t - b * g.n_tiles);
-    r.mt = 0;
-    int lo = 0, hi = g.E - 1;   // the expert with s_cum[e] <= b < s_cum[e + 1]
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_cum[mid + 1] > b)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    r.expert = lo;
-    const int first = static_cast<int>(b - s_cum[lo]) * kTileM;
-    r.row0 = static_cast<int64_t>(g.start[lo]) + first;
-    const int left = g.counts[lo] - first;
-    r.valid = left < kTileM ? left : kTileM;
-    r.kb = g.k_blocks;
-    r.tail = kBlockK;
-  }
-  return r;
+// Reports experts whose numbers do not fit (they are left out).
+__device__ __forceinline__ void report_experts(const ExpertArgs& g) {
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < g.E; e += blockDim.x)
+      if (g.counts[e] != expert_rows(g, e)) set_status(g.status, MOE_ERR_INVALID_ARG);
 }
 
 __device__ __forceinline__ void bulk_wait_read_2() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
@@ -165,42 +146,489 @@ __device__ __forceinline__ void stage_row(uint8_t* tile, int lane, const uint4 (
   for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(tile + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) = o[v];
 }
 
-// ... or straight to its row in memory, `left` columns from there.
-__device__ __forceinline__ void store_row(uint16_t* dst, int64_t left, const uint4 (&o)[4]) {
-#pragma unroll
-  for (int v = 0; v < 4; ++v)
-    if (8 * v < left) reinterpret_cast<uint4*>(dst)[v] = o[v];
+// Two features of a token into a store tile: 64-byte rows, 64-byte swizzle.
+__device__ __forceinline__ void put_word(uint8_t* tile, int token, int word, uint32_t w) {
+  *reinterpret_cast<uint32_t*>(tile + token * 64 + (((word >> 2) ^ ((token >> 1) & 3)) << 4) + (word & 3) * 4) = w;
 }
 
-// 32 bf16 values of a row, zeros past `left`.
-__device__ __forceinline__ void load_row(const uint16_t* src, int64_t left, uint4 (&o)[4]) {
+// A filled store tile of kTok tokens to memory: by TMA when they all exist (the
+// map clips features past the end), else each lane copies its token's row
+// (dst: the first token's, `left` features from there).  Either way one bulk
+// group more, so that the groups count tiles.
+template <int kTok>
+__device__ __forceinline__ void store_tile(uint8_t* tile, const CUtensorMap* map, int rows, int lane, int c0, int c1,
+                                           int c2, uint16_t* dst, int64_t ld, int64_t left) {
+  if (rows >= kTok) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store_3d(map, tile, c0, c1, c2);
+  } else {
+    __syncwarp();
+    if (lane < rows) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v)
-    o[v] = 8 * v < left ? __ldg(reinterpret_cast<const uint4*>(src) + v) : make_uint4(0, 0, 0, 0);
+      for (int v = 0; v < 4; ++v)
+        if (8 * v < left)
+          *reinterpret_cast<uint4*>(dst + lane * ld + 8 * v) =
+              *reinterpret_cast<const uint4*>(tile + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4));
+    }
+    __syncwarp();
+  }
+  if (lane == 0) bulk_commit_group();
 }
-__device__ __forceinline__ float bf16_at(const uint4 (&o)[4], int i) {
-  const uint4 q = o[i >> 3];
-  const uint32_t w = ((i >> 1) & 3) == 0 ? q.x : ((i >> 1) & 3) == 1 ? q.y : ((i >> 1) & 3) == 2 ? q.z : q.w;
-  return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+
+__device__ __forceinline__ void swiglu_grad(float dh, float gate, float up, float* dg, float* du) {
+  const float s = 1.0f / (1.0f + __expf(-gate));
+  *dg = dh * up * s * (1.0f + gate * (1.0f - s));
+  *du = dh * gate * s;
 }
+
+// ---------------------------------------------------------------------------
+// Products of rows
+// ---------------------------------------------------------------------------
+constexpr int kRowsA = 128 * kBlockK * 2;            // this CTA's 128 features, 16 KB
+constexpr int kRowsB = 128 * kBlockK * 2;            // this CTA's half of at most 256 tokens, 16 KB
+constexpr int kTokens = 256;                         // tokens of a tile at most
+
+struct RowsTile {
+  int expert;
+  int64_t row0;   // first sorted row
+  int valid;      // tokens
+  int n;          // tokens of the MMA: valid rounded up to 32
+  int box;        // the map of x that loads half of them: 128 >> box rows
+  int ft;         // feature tile
+};
+
+__device__ __forceinline__ RowsTile rows_tile(const ExpertArgs& g, const int32_t* s_cum, int64_t t) {
+  RowsTile r;
+  int lo = 0, hi = g.E - 1;   // the expert whose tiles hold t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(s_cum[mid + 1]) * g.n_tiles > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  const int first = s_cum[lo], blocks = s_cum[lo + 1] - first, count = g.counts[lo];
+  // token blocks innermost: they share a weight tile while it is in L2
+  const int i = static_cast<int>(t - static_cast<int64_t>(first) * g.n_tiles);
+  r.ft = i / blocks;
+  const int b = i - r.ft * blocks;
+  const int tall = ((count + blocks - 1) / blocks + 31) & ~31;
+  r.expert = lo;
+  r.row0 = static_cast<int64_t>(g.start[lo]) + b * tall;
+  const int left = count - b * tall;
+  r.valid = left < tall ? left : tall;
+  r.n = (r.valid + 31) & ~31;
+  r.box = r.n > 128 ? 0 : r.n > 64 ? 1 : 2;
+  return r;
+}
+
+// The epilogue's lanes hold one feature of two tokens (a, b); the neighbour
+// lane^1 the next (or previous) feature of the same.  After the exchange an
+// even lane has both features of the first token, an odd lane of the second.
+__device__ __forceinline__ float2 pair_up(float a, float b, bool odd) {
+  const float x = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+  return odd ? make_float2(x, b) : make_float2(a, x);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// g and u of chunk c of a tile, arranged as pair_up leaves dh: word i of an even
+// (odd) lane holds two features of token 2i (2i + 1).  Zeros where there is none.
+__device__ __forceinline__ void load_gate_up(const ExpertArgs& g, const RowsTile& tl, int c, int64_t col, int64_t left,
+                                             int lane, uint32_t (&gw)[16], uint32_t (&uw)[16]) {
+  const int tok = c * 32 + (lane & 1);
+  const bool there = (lane & ~1) < left;
+  const uint16_t* src = g.gu + (tl.row0 + tok) * g.gu_ld + col + (lane & ~1);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    gw[i] = uw[i] = 0;
+    if (there && tok + 2 * i < tl.valid) {
+      gw[i] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * i * g.gu_ld));
+      uw[i] = __ldg(reinterpret_cast<const uint32_t*>(src + 2 * i * g.gu_ld + g.n_cols));
+    }
+  }
+}
+
+// Tensor maps of a rows launch.  x: the tokens in boxes of 128, 64 and 32 rows (a
+// tile takes the smallest that holds its half of the tokens: one copy per stage,
+// as more copies of fewer bytes are slower: 358 us in 32-row boxes, 300 us so,
+// at 16384 x 4096 x 4096); out: the output or its first half, out2: its second
+// half, h: kFwdSwiglu's third output.
+struct RowsMaps {
+  CUtensorMap w, x[3], out, out2, h;
+};
 
 template <ExpertOp kOp>
-__global__ void __launch_bounds__(kThreads, 1)
-    expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                       const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_h,
-                       const ExpertArgs g) {
+__global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
+    expert_rows_kernel(const __grid_constant__ RowsMaps maps, const ExpertArgs g) {
+  using F = Cfg<kOp>;
+  constexpr int kRowsStages = F::kStages, kEpiWarps = F::kEpiWarps, kThreads = F::kThreads;
+  constexpr int kFeatures = kOp == kFwdSwiglu ? 128 : 256;   // output features of a tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kOffTail);
+  uint64_t* empty = full + kRowsStages;
+  uint64_t* tfull = empty + kRowsStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint64_t* xchg = done + 1;   // kFwdSwiglu: the warps of g and of u
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + F::kOffTail + kTailHolder);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + F::kOffTail + kTailAbort);
+  int32_t* s_scan = reinterpret_cast<int32_t*>(smem + F::kOffTail + kTailScan);
+  int32_t* s_cum = reinterpret_cast<int32_t*>(smem + F::kOffTail + kTailCum);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRowsStages; ++s) {
+      mbar_init(&full[s], 1);     // (the even CTA's is used: its producer arrives, both CTAs' copies count)
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpiWarps);   // (the even CTA's: both CTAs' epilogue warps)
+    }
+    mbar_init(done, 1);
+    for (int q = 0; q < 4; ++q) mbar_init(&xchg[q], 64);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&maps.w);
+    prefetch_tensormap(&maps.x[0]);
+    prefetch_tensormap(&maps.out);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(holder, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  pdl_wait();
+  pdl_trigger();
+  {
+    // token blocks of the experts before each: a thread takes consecutive
+    // experts, and the threads' sums are scanned
+    const int per = (g.E + kThreads - 1) / kThreads;
+    const int e0 = threadIdx.x * per;
+    int sum = 0;
+    for (int e = e0; e < e0 + per && e < g.E; ++e) sum += (expert_rows(g, e) + kTokens - 1) / kTokens;
+    int x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int base = x - sum;
+    for (int w = 0; w < warp; ++w) base += s_scan[w];
+    for (int e = e0; e < e0 + per && e < g.E; ++e) {
+      s_cum[e] = base;
+      base += (expert_rows(g, e) + kTokens - 1) / kTokens;
+      if (e == g.E - 1) s_cum[g.E] = base;
+    }
+  }
+  report_experts(g);
+  tc_fence_before();
+  // both CTAs' barriers and tensor memory are ready before either is used
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const int64_t n_tiles = static_cast<int64_t>(s_cum[g.E]) * g.n_tiles;
+  const int64_t t0 = blockIdx.x >> 1, t_step = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < n_tiles && ok; t += t_step) {
+        const RowsTile tl = rows_tile(g, s_cum, t);
+        const uint32_t bytes = kRowsA + (kRowsB >> tl.box);
+        const int tok = static_cast<int>(tl.row0) + static_cast<int>(rank) * (tl.n / 2);
+        const int f = tl.ft * kFeatures + static_cast<int>(rank) * (kFeatures / 2);
+        for (int kb = 0; kb < g.k_blocks; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          uint8_t* a = smem + stage * (kRowsA + kRowsB);
+          uint8_t* b = a + kRowsA;
+          const uint32_t bar = mapa(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+          const int k = kb * kBlockK;
+          if constexpr (kOp == kFwd) {
+            tma_load_3d_pair(a, &maps.w, bar, k, f, tl.expert);
+          } else if constexpr (kOp == kFwdSwiglu) {
+            tma_load_3d_pair(a, &maps.w, bar, k, f, tl.expert);
+            tma_load_3d_pair(a + kRowsA / 2, &maps.w, bar, k, static_cast<int>(g.n_cols) + f, tl.expert);
+          } else {
+            tma_load_3d_pair(a, &maps.w, bar, f, k, tl.expert);
+            tma_load_3d_pair(a + kBoxBytes, &maps.w, bar, f + 64, k, tl.expert);
+          }
+          tma_load_3d_pair(b, &maps.x[tl.box], bar, k, tok, 0);
+          if (++stage == kRowsStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        // copies may still be on their way into this CTA's shared memory, and
+        // complete on the other CTA's barrier: leave them ample time
+        const uint64_t now = globaltimer_ns();
+        while (globaltimer_ns() - now < 2000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0 && lane == 0) {
+      constexpr bool kAMn = kOp == kDgrad || kOp == kDgradSwiglu;
+      int stage = 0, iter = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < n_tiles && ok; t += t_step, ++iter) {
+        const RowsTile tl = rows_tile(g, s_cum, t);
+        const uint32_t idesc = kIdesc | (kAMn ? kAMnMajor : 0u) | idesc_mn(256, tl.n);
+        const int acc = iter & 1;
+        if (!mbar_wait_cluster_bounded(&tempty[acc], ((iter >> 1) & 1) ^ 1, abort_flag, g.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * kTokens);
+        for (int kb = 0; kb < g.k_blocks; ++kb) {
+          if (!mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + stage * (kRowsA + kRowsB));
+          const uint64_t ad = smem_desc(a, kAMn ? kBoxBytes : 16, 1024, kSwizzle128B);
+          const uint64_t bd = smem_desc(a + kRowsA, 16, 1024, kSwizzle128B);
+          // 16 reduction elements on: 32 bytes along a K-major row, 16 rows of
+          // 128 bytes down an MN-major box
+          constexpr uint64_t astep = (kAMn ? 2048 : 32) >> 4, bstep = 32 >> 4;
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            mma_bf16_pair(d, ad + astep * k, bd + bstep * k, idesc, !(kb == 0 && k == 0));
+          tc_commit_pair(&empty[stage]);
+          if (++stage == kRowsStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair(&tfull[acc]);
+      }
+      if (!ok) {
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // all issued tensor-core work finished before the tensor memory is released
+      tc_commit_pair(done);
+      const int never = 0;
+      mbar_wait_bounded(done, 0, &never, g.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    const int quad = warp & 3;
+    const bool odd = lane & 1;
+    const int half = (warp - 2) >> 2;        // eight warps: each takes every other chunk
+    uint8_t* stg = smem + F::kOffStg + (warp - 2) * F::kStgBytes;
+    int iter = 0;
+    uint32_t slot = 0, met = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < n_tiles; t += t_step, ++iter) {
+      const RowsTile tl = rows_tile(g, s_cum, t);
+      const int acc = iter & 1;
+      // this warp's 32 features, from col (kFwdSwiglu: quads 0 and 1 hold g, 2 and 3 the same features' u)
+      const int64_t col = static_cast<int64_t>(tl.ft) * kFeatures + static_cast<int>(rank) * (kFeatures / 2) +
+                          (kOp == kFwdSwiglu ? quad & 1 : quad) * 32;
+      const int64_t left = g.n_cols - col;   // features there are from col
+      const int chunks = tl.n / 32;
+      constexpr int kStep = kEpiWarps / 4;
+      // kDgradSwiglu: g and u as pair_up leaves dh, a chunk ahead of it (the
+      // first while the MMAs run, and the others brought into L2 then)
+      uint32_t gw[kOp == kDgradSwiglu ? 16 : 1], uw[kOp == kDgradSwiglu ? 16 : 1];
+      if constexpr (kOp == kDgradSwiglu) {
+        load_gate_up(g, tl, half, col, left, lane, gw, uw);
+        for (int c = half + kStep; c < chunks; c += kStep)
+          if (c * 32 + lane < tl.valid && left > 0) {
+            const uint16_t* src = g.gu + (tl.row0 + c * 32 + lane) * g.gu_ld + col;
+            prefetch_l2(src);
+            prefetch_l2(src + g.n_cols);
+          }
+      }
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns))) {
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t taddr = tmem + static_cast<uint32_t>(acc * kTokens) + (static_cast<uint32_t>(quad * 32) << 16);
+      if (half >= chunks) {   // nothing here for this warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+      }
+      for (int c = half; c < chunks; c += kStep) {
+        const int tok = c * 32;
+        const int64_t row = tl.row0 + tok;
+        const int rows = min(32, tl.valid - tok);
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + tok, v);
+        uint32_t ng[kOp == kDgradSwiglu ? 16 : 1], nu[kOp == kDgradSwiglu ? 16 : 1];
+        if constexpr (kOp == kDgradSwiglu) load_gate_up(g, tl, c + kStep, col, left, lane, ng, nu);
+        tmem_ld_wait();
+        if (c + kStep >= chunks) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+        }
+        if (left <= 0) continue;   // warp-uniform
+        if constexpr (kOp == kFwd || kOp == kDgrad) {
+          if (lane == 0) bulk_wait_read_2();   // the store from this tile three chunks ago has read it
+          __syncwarp();
+          uint8_t* tile = stg + slot * kStgTile;
+          slot = slot == F::kTiles - 1 ? 0 : slot + 1;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 p = pair_up(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), odd);
+            put_word(tile, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
+          }
+          store_tile<32>(tile, &maps.out, rows, lane, static_cast<int>(col), 0, static_cast<int>(row),
+                     g.out + row * g.out_ld + col, g.out_ld, left);
+        } else if constexpr (kOp == kDgradSwiglu) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 dh = pair_up(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), odd);
+            const float2 gate = unpack_bf16x2(gw[i]), up = unpack_bf16x2(uw[i]);
+            float2 dg, du;
+            swiglu_grad(dh.x, gate.x, up.x, &dg.x, &du.x);
+            swiglu_grad(dh.y, gate.y, up.y, &dg.y, &du.y);
+            put_word(stg, 2 * i + odd, lane >> 1, pack_bf16x2(dg.x, dg.y));
+            put_word(stg + kStgTile, 2 * i + odd, lane >> 1, pack_bf16x2(du.x, du.y));
+          }
+          uint16_t* dst = g.out + row * g.out_ld + col;
+          store_tile<32>(stg, &maps.out, rows, lane, static_cast<int>(col), 0, static_cast<int>(row), dst, g.out_ld, left);
+          store_tile<32>(stg + kStgTile, &maps.out2, rows, lane, static_cast<int>(col), 0, static_cast<int>(row),
+                     dst + g.n_cols, g.out_ld, left);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            gw[i] = ng[i];
+            uw[i] = nu[i];
+          }
+        } else {
+          // the g warp forms h of the chunk's first 16 tokens, the u warp of
+          // the others: each gives the other its half (two buffers in turn,
+          // so one meeting per chunk is enough)
+          const bool is_up = quad >= 2;
+          float* mine = reinterpret_cast<float*>(stg + kXchg) + (met & 1) * 512;
+          const float* theirs = reinterpret_cast<const float*>(smem + F::kOffStg + (((warp - 2) ^ 2) * F::kStgBytes) + kXchg) +
+                                (met & 1) * 512;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = __uint_as_float(is_up ? v[i] : v[16 + i]);
+          mbar_arrive(&xchg[2 * half + (quad & 1)]);
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          if (g.out) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 p = pair_up(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), odd);
+              put_word(stg, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
+            }
+            store_tile<32>(stg, is_up ? &maps.out2 : &maps.out, rows, lane, static_cast<int>(col), 0, static_cast<int>(row),
+                           g.out + row * g.out_ld + (is_up ? g.n_cols : 0) + col, g.out_ld, left);
+          }
+          const bool here = mbar_wait_bounded(&xchg[2 * half + (quad & 1)], met & 1, abort_flag, g.timeout_ns);
+          if (!__all_sync(0xFFFFFFFFu, here)) {
+            ok = false;
+            break;
+          }
+          ++met;
+          uint8_t* h_tile = stg + kStgTile;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x0 = theirs[2 * i * 32 + lane], x1 = theirs[(2 * i + 1) * 32 + lane];
+            const float h0 = is_up ? silu_mul(x0, __uint_as_float(v[16 + 2 * i])) : silu_mul(__uint_as_float(v[2 * i]), x0);
+            const float h1 = is_up ? silu_mul(x1, __uint_as_float(v[17 + 2 * i]))
+                                   : silu_mul(__uint_as_float(v[2 * i + 1]), x1);
+            const float2 p = pair_up(h0, h1, odd);
+            put_word(h_tile, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
+          }
+          const int h0 = is_up ? 16 : 0;
+          store_tile<16>(h_tile, &maps.h, rows - h0, lane, static_cast<int>(col), 0, static_cast<int>(row) + h0,
+                         g.h + (row + h0) * g.h_ld + col, g.h_ld, left);
+        }
+      }
+      if (!ok) {
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+    }
+    if (lane == 0) bulk_wait_all();   // this warp's stores have completed
+  }
+  // neither CTA leaves while the other's copies, MMAs or arrivals may reach it
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the weights
+// ---------------------------------------------------------------------------
+constexpr int kTileM = 128;
+constexpr int kTileN = 256;
+constexpr int kABytes = kTileM * kBlockK * 2;        // 16 KB
+constexpr int kBBytes = kTileN * kBlockK * 2;        // 32 KB
+static_assert(kABytes + kBBytes == Cfg<kWgrad>::kStage, "stage");
+
+struct WgradTile {
+  int expert;
+  int64_t row0;   // the expert's first sorted row
+  int mt, nt;     // output row and column tile
+  int kb;         // reduction blocks
+  int tail;       // rows of the last one
+};
+
+__device__ __forceinline__ WgradTile wgrad_tile(const ExpertArgs& g, int64_t t) {
+  WgradTile r;
+  const int64_t per = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
+  r.expert = static_cast<int>(t / per);
+  const int64_t i = t - r.expert * per;
+  r.mt = static_cast<int>(i / g.n_tiles);
+  r.nt = static_cast<int>(i - static_cast<int64_t>(r.mt) * g.n_tiles);
+  const int n = expert_rows(g, r.expert);
+  r.row0 = g.start[r.expert];
+  r.kb = (n + kBlockK - 1) / kBlockK;
+  r.tail = n - (r.kb - 1) * kBlockK;
+  return r;
+}
+
+__global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
+    expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const __grid_constant__ CUtensorMap map_out, const ExpertArgs g) {
+  using F = Cfg<kWgrad>;
+  constexpr int kStages = F::kStages, kEpiWarps = F::kEpiWarps;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kOffTail);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = full + 2 * kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffAbort);
-  int32_t* s_scan = reinterpret_cast<int32_t*>(smem + kOffScan);
-  int32_t* s_cum = reinterpret_cast<int32_t*>(smem + kOffCum);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + F::kOffTail + kTailHolder);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + F::kOffTail + kTailAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -225,38 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  // row blocks of the experts before each, from the counts: a thread takes
-  // consecutive experts, and the threads' sums are scanned
-  if constexpr (kOp != kWgrad) {
-    const int per = (g.E + kThreads - 1) / kThreads;
-    const int e0 = threadIdx.x * per;
-    int sum = 0;
-    for (int e = e0; e < e0 + per && e < g.E; ++e) sum += (expert_rows(g, e) + kTileM - 1) / kTileM;
-    int x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    int base = x - sum;
-    for (int w = 0; w < warp; ++w) base += s_scan[w];
-    for (int e = e0; e < e0 + per && e < g.E; ++e) {
-      s_cum[e] = base;
-      base += (expert_rows(g, e) + kTileM - 1) / kTileM;
-      if (e == g.E - 1) s_cum[g.E] = base;
-    }
-  }
-  if (blockIdx.x == 0)   // numbers that do not fit: reported, and the expert left out
-    for (int e = threadIdx.x; e < g.E; e += kThreads)
-      if (g.counts[e] != expert_rows(g, e)) set_status(g.status, MOE_ERR_INVALID_ARG);
+  report_experts(g);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  const int64_t n_tiles =
-      kOp == kWgrad ? static_cast<int64_t>(g.E) * g.m_tiles * g.n_tiles : static_cast<int64_t>(s_cum[g.E]) * g.n_tiles;
+  const int64_t n_tiles = static_cast<int64_t>(g.E) * g.m_tiles * g.n_tiles;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
@@ -265,39 +667,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-        const Tile tl = tile_at<kOp>(g, s_cum, t);
+        const WgradTile tl = wgrad_tile(g, t);
         for (int kb = 0; kb < tl.kb; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns)) {
             ok = false;
             break;
           }
-          uint8_t* a = smem + kOffA + stage * kABytes;
-          uint8_t* b = smem + kOffB + stage * kBBytes;
+          uint8_t* a = smem + stage * (kABytes + kBBytes);
+          uint8_t* b = a + kABytes;
           uint64_t* bar = &full[stage];
           mbar_arrive_expect_tx(bar, kABytes + kBBytes);
           const int k = kb * kBlockK;
-          if constexpr (kOp == kWgrad) {
-            const int row = static_cast<int>(tl.row0) + k;
+          const int row = static_cast<int>(tl.row0) + k;
 #pragma unroll
-            for (int i = 0; i < kTileM / 64; ++i)
-              tma_load_3d(a + i * kBoxBytes, &map_a, bar, tl.mt * kTileM + 64 * i, row, 0);
+          for (int i = 0; i < kTileM / 64; ++i)
+            tma_load_3d(a + i * kBoxBytes, &map_a, bar, tl.mt * kTileM + 64 * i, row, 0);
 #pragma unroll
-            for (int i = 0; i < kTileN / 64; ++i)
-              tma_load_3d(b + i * kBoxBytes, &map_b, bar, tl.nt * kTileN + 64 * i, row, 0);
-          } else {
-            tma_load_3d(a, &map_a, bar, k, static_cast<int>(tl.row0), 0);
-            if constexpr (kOp == kFwd) {
-              tma_load_3d(b, &map_b, bar, k, tl.nt * kTileN, tl.expert);
-            } else if constexpr (kOp == kFwdSwiglu) {
-              // gate rows, and the up rows I further down
-              tma_load_3d(b, &map_b, bar, k, tl.nt * 128, tl.expert);
-              tma_load_3d(b + kBBytes / 2, &map_b, bar, k, static_cast<int>(g.n_cols) + tl.nt * 128, tl.expert);
-            } else {
-#pragma unroll
-              for (int i = 0; i < kTileN / 64; ++i)
-                tma_load_3d(b + i * kBoxBytes, &map_b, bar, tl.nt * kTileN + 64 * i, k, tl.expert);
-            }
-          }
+          for (int i = 0; i < kTileN / 64; ++i)
+            tma_load_3d(b + i * kBoxBytes, &map_b, bar, tl.nt * kTileN + 64 * i, row, 0);
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
@@ -319,14 +706,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    constexpr bool kAMn = kOp == kWgrad;
-    constexpr bool kBMn = kOp == kDgrad || kOp == kDgradSwiglu || kOp == kWgrad;
-    constexpr uint32_t idesc = kIdesc | (kAMn ? kAMnMajor : 0u) | (kBMn ? kBMnMajor : 0u);
+    constexpr uint32_t idesc = kIdesc | kAMnMajor | kBMnMajor | idesc_mn(kTileM, kTileN);
     int stage = 0, iter = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-      const Tile tl = tile_at<kOp>(g, s_cum, t);
+      const WgradTile tl = wgrad_tile(g, t);
       if (tl.kb == 0) continue;
       const int acc = iter & 1;
       ok = __all_sync(0xFFFFFFFFu,
@@ -338,10 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < tl.kb; ++kb) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns));
         if (!ok) break;
-        uint8_t* a = smem + kOffA + stage * kABytes;
-        uint8_t* b = smem + kOffB + stage * kBBytes;
+        uint8_t* a = smem + stage * (kABytes + kBBytes);
+        uint8_t* b = a + kABytes;
         int steps = kBlockK / 16;
-        if (kOp == kWgrad && kb == tl.kb - 1 && tl.tail < kBlockK) {
+        if (kb == tl.kb - 1 && tl.tail < kBlockK) {
           // the expert's last rows: whole steps of 16 rows past its end are
           // left out, the rest of the last step is cleared in both operands
           // (they are consecutive in shared memory as 2 + 4 boxes of
@@ -358,12 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t ad = smem_desc(smem_u32(a), kAMn ? kBoxBytes : 16, 1024, kSwizzle128B);
-          const uint64_t bd = smem_desc(smem_u32(b), kBMn ? kBoxBytes : 16, 1024, kSwizzle128B);
-          // 16 reduction elements on: 32 bytes along a K-major row, 16 rows of
-          // 128 bytes down an MN-major box
-          constexpr uint64_t astep = (kAMn ? 2048 : 32) >> 4, bstep = (kBMn ? 2048 : 32) >> 4;
-          for (int k = 0; k < steps; ++k) mma_bf16(d, ad + astep * k, bd + bstep * k, idesc, !(kb == 0 && k == 0));
+          const uint64_t ad = smem_desc(smem_u32(a), kBoxBytes, 1024, kSwizzle128B);
+          const uint64_t bd = smem_desc(smem_u32(b), kBoxBytes, 1024, kSwizzle128B);
+          // 16 reduction rows on: 16 rows of 128 bytes down the boxes
+          for (int k = 0; k < steps; ++k)
+            mma_bf16(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(kb == 0 && k == 0));
           tc_commit(&empty[stage]);
           if (kb == tl.kb - 1) tc_commit(&tfull[acc]);
         }
@@ -388,11 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------------ epilogue
     const int quad = warp & 3;
-    uint8_t* stg = smem + kOffStg + (warp - 2) * kStgPerWarp * kStgTile;
+    uint8_t* stg = smem + F::kOffStg + (warp - 2) * F::kStgBytes;
     int iter = 0;
     uint32_t slot = 0;
     for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-      const Tile tl = tile_at<kOp>(g, s_cum, t);
+      const WgradTile tl = wgrad_tile(g, t);
       const int acc = iter & 1;
       if (tl.kb > 0) {
         const bool got = mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns);
@@ -405,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++iter;
       }
       const uint32_t taddr = tmem + static_cast<uint32_t>(acc * kTileN) + (static_cast<uint32_t>(quad * 32) << 16);
-      if constexpr (kOp == kWgrad) {
+      {
         const int64_t r0 = static_cast<int64_t>(tl.mt) * kTileM + quad * 32;
         const int64_t col0 = static_cast<int64_t>(tl.nt) * kTileN;
 #pragma unroll 1
@@ -439,108 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_store_3d(&map_out, tile, static_cast<int>(col0) + c * 32, static_cast<int>(r0), tl.expert);
             bulk_commit_group();
           }
-          slot = slot == kStgPerWarp - 1 ? 0 : slot + 1;
-        }
-        continue;
-      } else {
-        const int r = quad * 32 + lane;
-        const bool row_ok = r < tl.valid;
-        const bool whole = quad * 32 + 32 <= tl.valid;   // all of this warp's rows exist
-        const bool none = quad * 32 >= tl.valid;
-        const int64_t row = tl.row0 + r;
-        const int row_w = static_cast<int>(tl.row0) + quad * 32;
-        constexpr int kChunks = kOp == kFwdSwiglu ? 4 : kTileN / 32;
-        const int64_t col0 = static_cast<int64_t>(tl.nt) * (kOp == kFwdSwiglu ? 128 : kTileN);
-#pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
-          const int64_t col = col0 + c * 32, left = g.n_cols - col;
-          const bool last = c == kChunks - 1;
-          const bool skip = none || left <= 0;   // warp-uniform
-          uint4 gq[4], uq[4];
-          if (kOp == kDgradSwiglu && !skip && row_ok) {
-            load_row(g.gu + row * g.gu_ld + col, left, gq);
-            load_row(g.gu + row * g.gu_ld + g.n_cols + col, left, uq);
-          }
-          uint32_t v[32], u[kOp == kFwdSwiglu ? 32 : 1];
-          if (!skip) {
-            tmem_ld_32x32b_x32(taddr + c * 32, v);
-            if constexpr (kOp == kFwdSwiglu) tmem_ld_32x32b_x32(taddr + 128 + c * 32, u);
-            tmem_ld_wait();
-          }
-          if (last) {
-            tc_fence_before();
-            mbar_arrive(&tempty[acc]);
-          }
-          if (skip) continue;
-          if constexpr (kOp == kFwd || kOp == kDgrad) {
-            float f[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-            uint4 o[4];
-            pack32(f, o);
-            if (whole) {
-              if (lane == 0) bulk_wait_read_2();
-              __syncwarp();
-              uint8_t* tile = stg + slot * kStgTile;
-              stage_row(tile, lane, o);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(&map_out, tile, static_cast<int>(col), 0, row_w);
-                bulk_commit_group();
-              }
-              slot = slot == kStgPerWarp - 1 ? 0 : slot + 1;
-            } else if (row_ok) {
-              store_row(g.out + row * g.out_ld + col, left, o);
-            }
-          } else {
-            // two output halves (g, u or dg, du), and h
-            float f0[32], f1[32], f2[kOp == kFwdSwiglu ? 32 : 1];
-            if constexpr (kOp == kFwdSwiglu) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                f0[i] = __uint_as_float(v[i]);
-                f1[i] = __uint_as_float(u[i]);
-                f2[i] = silu_mul(f0[i], f1[i]);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float gate = bf16_at(gq, i), up = bf16_at(uq, i), dh = __uint_as_float(v[i]);
-                const float s = 1.0f / (1.0f + __expf(-gate));
-                f0[i] = dh * up * s * (1.0f + gate * (1.0f - s));
-                f1[i] = dh * gate * s;
-              }
-            }
-            uint4 o0[4], o1[4], o2[4];
-            pack32(f0, o0);
-            pack32(f1, o1);
-            if constexpr (kOp == kFwdSwiglu) pack32(f2, o2);
-            if (whole) {
-              if (lane == 0) bulk_wait_read_all();
-              __syncwarp();
-              stage_row(stg, lane, o0);
-              stage_row(stg + kStgTile, lane, o1);
-              if constexpr (kOp == kFwdSwiglu) stage_row(stg + 2 * kStgTile, lane, o2);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (g.out) {
-                  tma_store_3d(&map_out, stg, static_cast<int>(col), 0, row_w);
-                  tma_store_3d(&map_out, stg + kStgTile, static_cast<int>(col), 1, row_w);
-                }
-                if constexpr (kOp == kFwdSwiglu)
-                  tma_store_3d(&map_h, stg + 2 * kStgTile, static_cast<int>(col), 0, row_w);
-                bulk_commit_group();
-              }
-            } else if (row_ok) {
-              if (g.out) {
-                store_row(g.out + row * g.out_ld + col, left, o0);
-                store_row(g.out + row * g.out_ld + g.n_cols + col, left, o1);
-              }
-              if constexpr (kOp == kFwdSwiglu) store_row(g.h + row * g.h_ld + col, left, o2);
-            }
-          }
+          slot = slot == F::kTiles - 1 ? 0 : slot + 1;
         }
       }
     }
@@ -553,22 +836,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+int num_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// max_tiles: at least the tiles of any split of the rows among the experts.
 template <ExpertOp kOp>
-cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const CUtensorMap& h,
-                   const ExpertArgs& g, int64_t max_tiles, cudaStream_t s) {
+cudaError_t launch_rows(const RowsMaps& maps, const ExpertArgs& g, int64_t max_tiles, cudaStream_t s) {
+  static int pairs = 0;   // CTA pairs that fit on the device at once
+  using F = Cfg<kOp>;
+  if (pairs == 0) {
+    cudaError_t e =
+        cudaFuncSetAttribute(expert_rows_kernel<kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(F::kThreads);
+    cfg.dynamicSmemBytes = F::kSmem;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, expert_rows_kernel<kOp>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    pairs = clusters;
+  }
+  const int grid = 2 * static_cast<int>(max_tiles < pairs ? max_tiles : pairs);
+  return launch_pdl_cluster(expert_rows_kernel<kOp>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, maps, g);
+}
+
+cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const ExpertArgs& g,
+                         int64_t tiles, cudaStream_t s) {
   static bool attr_set = false;
   if (!attr_set) {
     const cudaError_t e =
-        cudaFuncSetAttribute(expert_gemm_kernel<kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        cudaFuncSetAttribute(expert_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kWgrad>::kSmem);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int grid = static_cast<int>(max_tiles < sms ? max_tiles : sms);
-  return launch_pdl(expert_gemm_kernel<kOp>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, b, out, h, g);
+  const int sms = num_sms();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  return launch_pdl(expert_wgrad_kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(Cfg<kWgrad>::kThreads),
+                    Cfg<kWgrad>::kSmem, s, a, b, out, g);
 }
 
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -587,11 +905,19 @@ moe_status_t weights_map(CUtensorMap* m, const void* p, int64_t E, int64_t n, in
   const uint32_t box[3] = {64, box_rows, 1};
   return encode_tiled_map(m, p, kBf16, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// [rows][halves][cols] output with row stride ld, stored 32 rows x 32 columns at a time.
-moe_status_t out_map(CUtensorMap* m, const void* p, int64_t rows, int64_t halves, int64_t cols, int64_t ld) {
-  const uint64_t d[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(halves), static_cast<uint64_t>(rows)};
-  const uint64_t st[2] = {static_cast<uint64_t>(cols) * 2, static_cast<uint64_t>(ld) * 2};
-  const uint32_t box[3] = {32, 1, 32};
+// x of a rows launch: boxes of 128, 64 and 32 rows.
+moe_status_t token_maps(RowsMaps* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  for (int i = 0; i < 3; ++i) {
+    const moe_status_t st = rows_map(&m->x[i], p, rows, cols, ld, 128 >> i);
+    if (st != MOE_OK) return st;
+  }
+  return MOE_OK;
+}
+// [rows][1][cols] output with row stride ld, stored box_rows rows x 32 columns at a time.
+moe_status_t out_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows = 32) {
+  const uint64_t d[3] = {static_cast<uint64_t>(cols), 1, static_cast<uint64_t>(rows)};
+  const uint64_t st[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(ld) * 2};
+  const uint32_t box[3] = {32, 1, box_rows};
   return encode_tiled_map(m, p, kBf16, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
@@ -635,8 +961,8 @@ ExpertArgs expert_args(int64_t rows, int32_t E, const int32_t* start, const int3
 
 int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
 
-// Row blocks of any split of `rows` rows among E experts, at most.
-int64_t max_blocks(int64_t rows, int32_t E) { return rows / kTileM + E; }
+// Token blocks of any split of `rows` rows among E experts, at most.
+int64_t max_blocks(int64_t rows, int32_t E) { return rows / kTokens + E; }
 
 moe_status_t as_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -656,17 +982,18 @@ moe_status_t moe_expert_gemm(const void* x, int64_t x_ld, int64_t rows, const vo
   if (!w) return MOE_ERR_INVALID_ARG;
   if (off16(w)) return MOE_ERR_MISALIGNED;
   if (rows == 0) return MOE_OK;
-  CUtensorMap a, b, o;
-  if ((st = rows_map(&a, x, rows, C, x_ld, kTileM)) != MOE_OK) return st;
-  if ((st = weights_map(&b, w, E, N, C, kTileN)) != MOE_OK) return st;
-  if ((st = out_map(&o, y, rows, 1, N, y_ld)) != MOE_OK) return st;
+  RowsMaps m;
+  if ((st = token_maps(&m, x, rows, C, x_ld)) != MOE_OK) return st;
+  if ((st = weights_map(&m.w, w, E, N, C, 128)) != MOE_OK) return st;
+  if ((st = out_map(&m.out, y, rows, N, y_ld)) != MOE_OK) return st;
+  m.out2 = m.h = m.out;
   ExpertArgs g = expert_args(rows, E, start, counts, status);
-  g.n_tiles = ceil_div(N, kTileN);
+  g.n_tiles = ceil_div(N, 256);
   g.k_blocks = ceil_div(C, kBlockK);
   g.n_cols = N;
   g.out = static_cast<uint16_t*>(y);
   g.out_ld = y_ld;
-  return as_status(launch<kFwd>(a, b, o, o, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
+  return as_status(launch_rows<kFwd>(m, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_expert_gemm_swiglu(const void* x, int64_t x_ld, int64_t rows, const void* w13, const int32_t* start,
@@ -679,12 +1006,13 @@ moe_status_t moe_expert_gemm_swiglu(const void* x, int64_t x_ld, int64_t rows, c
   if (gu && gu_ld < 2 * I) return MOE_ERR_INVALID_ARG;
   if (gu && (gu_ld % 8 || gu_ld > (int64_t(1) << 36))) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
-  CUtensorMap a, b, o, hm;
-  if ((st = rows_map(&a, x, rows, C, x_ld, kTileM)) != MOE_OK) return st;
-  if ((st = weights_map(&b, w13, E, 2 * I, C, 128)) != MOE_OK) return st;
-  if ((st = out_map(&hm, h, rows, 1, I, h_ld)) != MOE_OK) return st;
-  o = hm;
-  if (gu && (st = out_map(&o, gu, rows, 2, I, gu_ld)) != MOE_OK) return st;
+  RowsMaps m;
+  if ((st = token_maps(&m, x, rows, C, x_ld)) != MOE_OK) return st;
+  if ((st = weights_map(&m.w, w13, E, 2 * I, C, 64)) != MOE_OK) return st;
+  if ((st = out_map(&m.h, h, rows, I, h_ld, 16)) != MOE_OK) return st;
+  m.out = m.out2 = m.h;
+  if (gu && (st = out_map(&m.out, gu, rows, I, gu_ld)) != MOE_OK) return st;
+  if (gu && (st = out_map(&m.out2, static_cast<uint16_t*>(gu) + I, rows, I, gu_ld)) != MOE_OK) return st;
   ExpertArgs g = expert_args(rows, E, start, counts, status);
   g.n_tiles = ceil_div(I, 128);
   g.k_blocks = ceil_div(C, kBlockK);
@@ -694,7 +1022,7 @@ moe_status_t moe_expert_gemm_swiglu(const void* x, int64_t x_ld, int64_t rows, c
   g.h = static_cast<uint16_t*>(h);
   g.h_ld = h_ld;
   return as_status(
-      launch<kFwdSwiglu>(a, b, o, hm, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
+      launch_rows<kFwdSwiglu>(m, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_expert_gemm_dgrad(const void* dy, int64_t dy_ld, int64_t rows, const void* w, const int32_t* start,
@@ -705,17 +1033,18 @@ moe_status_t moe_expert_gemm_dgrad(const void* dy, int64_t dy_ld, int64_t rows, 
   if (!w) return MOE_ERR_INVALID_ARG;
   if (off16(w)) return MOE_ERR_MISALIGNED;
   if (rows == 0) return MOE_OK;
-  CUtensorMap a, b, o;
-  if ((st = rows_map(&a, dy, rows, N, dy_ld, kTileM)) != MOE_OK) return st;
-  if ((st = weights_map(&b, w, E, N, C, kBlockK)) != MOE_OK) return st;
-  if ((st = out_map(&o, dx, rows, 1, C, dx_ld)) != MOE_OK) return st;
+  RowsMaps m;
+  if ((st = token_maps(&m, dy, rows, N, dy_ld)) != MOE_OK) return st;
+  if ((st = weights_map(&m.w, w, E, N, C, kBlockK)) != MOE_OK) return st;
+  if ((st = out_map(&m.out, dx, rows, C, dx_ld)) != MOE_OK) return st;
+  m.out2 = m.h = m.out;
   ExpertArgs g = expert_args(rows, E, start, counts, status);
-  g.n_tiles = ceil_div(C, kTileN);
+  g.n_tiles = ceil_div(C, 256);
   g.k_blocks = ceil_div(N, kBlockK);
   g.n_cols = C;
   g.out = static_cast<uint16_t*>(dx);
   g.out_ld = dx_ld;
-  return as_status(launch<kDgrad>(a, b, o, o, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
+  return as_status(launch_rows<kDgrad>(m, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_expert_gemm_dgrad_swiglu(const void* dy, int64_t dy_ld, int64_t rows, const void* w2, const void* gu,
@@ -727,12 +1056,14 @@ moe_status_t moe_expert_gemm_dgrad_swiglu(const void* dy, int64_t dy_ld, int64_t
   if (!w2) return MOE_ERR_INVALID_ARG;
   if (off16(w2)) return MOE_ERR_MISALIGNED;
   if (rows == 0) return MOE_OK;
-  CUtensorMap a, b, o;
-  if ((st = rows_map(&a, dy, rows, N, dy_ld, kTileM)) != MOE_OK) return st;
-  if ((st = weights_map(&b, w2, E, N, I, kBlockK)) != MOE_OK) return st;
-  if ((st = out_map(&o, dgu, rows, 2, I, dgu_ld)) != MOE_OK) return st;
+  RowsMaps m;
+  if ((st = token_maps(&m, dy, rows, N, dy_ld)) != MOE_OK) return st;
+  if ((st = weights_map(&m.w, w2, E, N, I, kBlockK)) != MOE_OK) return st;
+  if ((st = out_map(&m.out, dgu, rows, I, dgu_ld)) != MOE_OK) return st;
+  if ((st = out_map(&m.out2, static_cast<uint16_t*>(dgu) + I, rows, I, dgu_ld)) != MOE_OK) return st;
+  m.h = m.out;
   ExpertArgs g = expert_args(rows, E, start, counts, status);
-  g.n_tiles = ceil_div(I, kTileN);
+  g.n_tiles = ceil_div(I, 256);
   g.k_blocks = ceil_div(N, kBlockK);
   g.n_cols = I;
   g.out = static_cast<uint16_t*>(dgu);
@@ -740,7 +1071,7 @@ moe_status_t moe_expert_gemm_dgrad_swiglu(const void* dy, int64_t dy_ld, int64_t
   g.gu = static_cast<const uint16_t*>(gu);
   g.gu_ld = gu_ld;
   return as_status(
-      launch<kDgradSwiglu>(a, b, o, o, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
+      launch_rows<kDgradSwiglu>(m, g, max_blocks(rows, E) * g.n_tiles, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, int64_t rows,
@@ -764,8 +1095,8 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
   g.m_tiles = ceil_div(N, kTileM);
   g.n_rows = N;
   g.n_cols = C;
-  return as_status(launch<kWgrad>(a, b, o, o, g, static_cast<int64_t>(E) * g.m_tiles * g.n_tiles,
-                                  static_cast<cudaStream_t>(stream)));
+  return as_status(launch_wgrad(a, b, o, g, static_cast<int64_t>(E) * g.m_tiles * g.n_tiles,
+                                static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
