@@ -60,7 +60,7 @@ constexpr int kBlockK = 64;                          // elements: 128 bytes, one
 constexpr int kBoxBytes = 64 * kBlockK * 2;          // an MN-major box: 64 x 64 elements
 constexpr int kStgTile = 32 * 64;                    // a store tile: 32 rows x 32 columns
 constexpr uint32_t kTmemCols = 512;
-constexpr int kXchg = 3 * 1024;                      // kFwdSwiglu: a warp's tile and a half, and from there twice 16
+constexpr int kXchg = 5 * 1024;                      // kFwdSwiglu: a warp's two and a half tiles, and from there 16
                                                      // tokens x 32 lanes in fp32
 constexpr int kMaxStages = 6, kMaxEpiWarps = 8;
 
@@ -83,7 +83,7 @@ struct Cfg {
   static constexpr int kEpiWarps = kAct ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kTiles = 3;                       // store tiles of an epilogue warp
-  static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 4 * 1024 : kTiles * kStgTile;
+  static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 2 * 1024 : kTiles * kStgTile;
   static constexpr int kOffStg = kStages * kStage;
   static constexpr int kOffTail = kOffStg + kEpiWarps * kStgBytes;
   static constexpr int kSmem = kOffTail + kTailBytes;
@@ -130,7 +130,11 @@ __device__ __forceinline__ void report_experts(const ExpertArgs& g) {
       if (g.counts[e] != expert_rows(g, e)) set_status(g.status, MOE_ERR_INVALID_ARG);
 }
 
-__device__ __forceinline__ void bulk_wait_read_2() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
+// All but this thread's last n bulk groups have read their shared memory.
+template <int n>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
+}
 
 __device__ __forceinline__ void pack32(const float (&f)[32], uint4 (&o)[4]) {
 #pragma unroll
@@ -176,10 +180,21 @@ __device__ __forceinline__ void store_tile(uint8_t* tile, const CUtensorMap* map
   if (lane == 0) bulk_commit_group();
 }
 
+// 1 / (1 + exp(-x)) by the hardware's base-2 exponential and reciprocal, both
+// within 2 ulp: the epilogue's arithmetic is issue-bound (an IEEE quotient costs
+// as much as the rest), and the result is rounded to bf16.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
 __device__ __forceinline__ void swiglu_grad(float dh, float gate, float up, float* dg, float* du) {
-  const float s = 1.0f / (1.0f + __expf(-gate));
-  *dg = dh * up * s * (1.0f + gate * (1.0f - s));
-  *du = dh * gate * s;
+  const float s = sigmoid_fast(gate);
+  const float ds = dh * s;
+  *dg = ds * up * fmaf(gate, 1.0f - s, 1.0f);
+  *du = ds * gate;
 }
 
 // ---------------------------------------------------------------------------
@@ -442,6 +457,14 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     int iter = 0;
     uint32_t slot = 0, met = 0;
     bool ok = true;
+    // the warp's next store tile, once the store from it three tiles ago has read it
+    auto next_tile = [&]() {
+      if (lane == 0) bulk_wait_read<F::kTiles - 1>();
+      __syncwarp();
+      uint8_t* tile = stg + slot * kStgTile;
+      slot = slot == F::kTiles - 1 ? 0 : slot + 1;
+      return tile;
+    };
     for (int64_t t = t0; t < n_tiles; t += t_step, ++iter) {
       const RowsTile tl = rows_tile(g, s_cum, t);
       const int acc = iter & 1;
@@ -490,10 +513,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
         }
         if (left <= 0) continue;   // warp-uniform
         if constexpr (kOp == kFwd || kOp == kDgrad) {
-          if (lane == 0) bulk_wait_read_2();   // the store from this tile three chunks ago has read it
-          __syncwarp();
-          uint8_t* tile = stg + slot * kStgTile;
-          slot = slot == F::kTiles - 1 ? 0 : slot + 1;
+          uint8_t* tile = next_tile();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 p = pair_up(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), odd);
@@ -502,22 +522,26 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
           store_tile<32>(tile, &maps.out, rows, lane, static_cast<int>(col), 0, static_cast<int>(row),
                      g.out + row * g.out_ld + col, g.out_ld, left);
         } else if constexpr (kOp == kDgradSwiglu) {
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
+          uint32_t dg[16];
+          uint8_t* du_tile = next_tile();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 dh = pair_up(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), odd);
             const float2 gate = unpack_bf16x2(gw[i]), up = unpack_bf16x2(uw[i]);
-            float2 dg, du;
-            swiglu_grad(dh.x, gate.x, up.x, &dg.x, &du.x);
-            swiglu_grad(dh.y, gate.y, up.y, &dg.y, &du.y);
-            put_word(stg, 2 * i + odd, lane >> 1, pack_bf16x2(dg.x, dg.y));
-            put_word(stg + kStgTile, 2 * i + odd, lane >> 1, pack_bf16x2(du.x, du.y));
+            float2 g2, u2;
+            swiglu_grad(dh.x, gate.x, up.x, &g2.x, &u2.x);
+            swiglu_grad(dh.y, gate.y, up.y, &g2.y, &u2.y);
+            dg[i] = pack_bf16x2(g2.x, g2.y);
+            put_word(du_tile, 2 * i + odd, lane >> 1, pack_bf16x2(u2.x, u2.y));
           }
           uint16_t* dst = g.out + row * g.out_ld + col;
-          store_tile<32>(stg, &maps.out, rows, lane, static_cast<int>(col), 0, static_cast<int>(row), dst, g.out_ld, left);
-          store_tile<32>(stg + kStgTile, &maps.out2, rows, lane, static_cast<int>(col), 0, static_cast<int>(row),
-                     dst + g.n_cols, g.out_ld, left);
+          store_tile<32>(du_tile, &maps.out2, rows, lane, static_cast<int>(col), 0, static_cast<int>(row),
+                         dst + g.n_cols, g.out_ld, left);
+          uint8_t* dg_tile = next_tile();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) put_word(dg_tile, 2 * i + odd, lane >> 1, dg[i]);
+          store_tile<32>(dg_tile, &maps.out, rows, lane, static_cast<int>(col), 0, static_cast<int>(row), dst, g.out_ld,
+                         left);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             gw[i] = ng[i];
@@ -525,40 +549,54 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
           }
         } else {
           // the g warp forms h of the chunk's first 16 tokens, the u warp of
-          // the others: each gives the other its half (two buffers in turn,
-          // so one meeting per chunk is enough)
+          // the others: each gives the other its half.  Their barrier takes
+          // turns: values written (even phases), values read (odd).
           const bool is_up = quad >= 2;
-          float* mine = reinterpret_cast<float*>(stg + kXchg) + (met & 1) * 512;
-          const float* theirs = reinterpret_cast<const float*>(smem + F::kOffStg + (((warp - 2) ^ 2) * F::kStgBytes) + kXchg) +
-                                (met & 1) * 512;
+          uint64_t* meet = &xchg[2 * half + (quad & 1)];
+          float* mine = reinterpret_cast<float*>(stg + kXchg);
+          const float* theirs =
+              reinterpret_cast<const float*>(smem + F::kOffStg + ((warp - 2) ^ 2) * F::kStgBytes + kXchg);
+          if (met > 0)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(meet, 1, abort_flag, g.timeout_ns));
+          if (!ok) break;
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = __uint_as_float(is_up ? v[i] : v[16 + i]);
-          mbar_arrive(&xchg[2 * half + (quad & 1)]);
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
+          mbar_arrive(meet);
+          // the last bulk groups are, latest first: h, g or u of the chunk
+          // before, and of the one before that, whose g or u tile is taken now
           if (g.out) {
+            if (lane == 0) bulk_wait_read<2>();
+            __syncwarp();
+            uint8_t* tile = stg + (met & 1) * kStgTile;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 p = pair_up(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), odd);
-              put_word(stg, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
+              put_word(tile, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
             }
-            store_tile<32>(stg, is_up ? &maps.out2 : &maps.out, rows, lane, static_cast<int>(col), 0, static_cast<int>(row),
-                           g.out + row * g.out_ld + (is_up ? g.n_cols : 0) + col, g.out_ld, left);
+            store_tile<32>(tile, is_up ? &maps.out2 : &maps.out, rows, lane, static_cast<int>(col), 0,
+                           static_cast<int>(row), g.out + row * g.out_ld + (is_up ? g.n_cols : 0) + col, g.out_ld, left);
           }
-          const bool here = mbar_wait_bounded(&xchg[2 * half + (quad & 1)], met & 1, abort_flag, g.timeout_ns);
-          if (!__all_sync(0xFFFFFFFFu, here)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(meet, 0, abort_flag, g.timeout_ns));
+          if (!ok) break;
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = theirs[i * 32 + lane];
+          mbar_arrive(meet);
           ++met;
-          uint8_t* h_tile = stg + kStgTile;
+          // h's tile is single: its last store has read it
+          if (lane == 0) g.out ? bulk_wait_read<1>() : bulk_wait_read<0>();
+          __syncwarp();
+          uint8_t* h_tile = stg + 2 * kStgTile;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float x0 = theirs[2 * i * 32 + lane], x1 = theirs[(2 * i + 1) * 32 + lane];
-            const float h0 = is_up ? silu_mul(x0, __uint_as_float(v[16 + 2 * i])) : silu_mul(__uint_as_float(v[2 * i]), x0);
-            const float h1 = is_up ? silu_mul(x1, __uint_as_float(v[17 + 2 * i]))
-                                   : silu_mul(__uint_as_float(v[2 * i + 1]), x1);
-            const float2 p = pair_up(h0, h1, odd);
+            float hv[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int k = 2 * i + j;
+              const float gate = is_up ? x[k] : __uint_as_float(v[k]), up = is_up ? __uint_as_float(v[16 + k]) : x[k];
+              hv[j] = gate * sigmoid_fast(gate) * up;
+            }
+            const float2 p = pair_up(hv[0], hv[1], odd);
             put_word(h_tile, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
           }
           const int h0 = is_up ? 16 : 0;
@@ -812,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
           if (r0 >= g.n_rows || col0 + c * 32 >= g.n_cols) continue;   // warp-uniform
           uint4 o[4];
           pack32(f, o);
-          if (lane == 0) bulk_wait_read_2();   // the store from this tile three chunks ago has read it
+          if (lane == 0) bulk_wait_read<2>();   // the store from this tile three chunks ago has read it
           __syncwarp();
           uint8_t* tile = stg + slot * kStgTile;
           stage_row(tile, lane, o);
