@@ -400,28 +400,29 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr bool kAMn = kOp == kDgrad || kOp == kDgradSwiglu;
+      const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const int k_blocks = g.k_blocks;
       int stage = 0, iter = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int64_t t = t0; t < n_tiles && ok; t += t_step, ++iter) {
         const RowsTile tl = rows_tile(g, s_cum, t);
-        const uint32_t idesc = kIdesc | (kAMn ? kAMnMajor : 0u) | idesc_mn(256, tl.n);
+        const uint32_t idesc =
+            kIdesc | (kAMn ? kAMnMajor : 0u) | idesc_mn(256, __shfl_sync(0xFFFFFFFFu, tl.n, 0));
         const int acc = iter & 1;
-        if (!mbar_wait_cluster_bounded(&tempty[acc], ((iter >> 1) & 1) ^ 1, abort_flag, g.timeout_ns)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait_cluster_bounded(&tempty[acc], ((iter >> 1) & 1) ^ 1, abort_flag, g.timeout_ns));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * kTokens);
-        for (int kb = 0; kb < g.k_blocks; ++kb) {
-          if (!mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns)) {
-            ok = false;
-            break;
-          }
+        const uint32_t d = tm + static_cast<uint32_t>(acc * kTokens);
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + stage * (kRowsA + kRowsB));
+          const uint32_t a = base + stage * (kRowsA + kRowsB);
           const uint64_t ad = smem_desc(a, kAMn ? kBoxBytes : 16, 1024, kSwizzle128B);
           const uint64_t bd = smem_desc(a + kRowsA, 16, 1024, kSwizzle128B);
           // 16 reduction elements on: 32 bytes along a K-major row, 16 rows of
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
         if (!ok) break;
         tc_commit_pair(&tfull[acc]);
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_status(g.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
       }
