@@ -33,12 +33,12 @@
 // the warps of a feature's g and of its u hand each other half of a chunk's
 // tokens and form h of the other half.
 //
-// Weights' gradient (kWgrad).  dW = dy^T x, a tile of 128 x 256 on one CTA, both
-// operands MN-major (64 x 64 boxes, no transposed copies), summed over the
-// expert's rows 64 at a time.  Rows beyond the expert's in the last block are
-// cleared in shared memory before the product, so whatever lies there, NaN
-// included, does not count.  (In the other products such rows only make output
-// rows that are not stored.)
+// Weights' gradient (kWgrad).  dW = dy^T x, a tile of 256 x at most 256 on a CTA
+// pair, both operands MN-major (64 x 64 boxes, no transposed copies), summed
+// over the expert's rows 64 at a time.  Rows beyond the expert's in the last
+// block are cleared in both CTAs' shared memory before the product, so whatever
+// lies there, NaN included, does not count.  (In the other products such rows
+// only make output rows that are not stored.)
 //
 // Both: one persistent CTA per SM: warp 0 TMA producer, warp 1 MMA issue, warps
 // 2-5 epilogue (one per 32 accumulator lanes, independent of one another), two
@@ -65,7 +65,8 @@ constexpr int kXchg = 5 * 1024;                      // kFwdSwiglu: a warp's two
 constexpr int kMaxStages = 6, kMaxEpiWarps = 8;
 
 // Shared memory: the stages, the epilogue warps' tiles, then the same for all.
-constexpr int kNumBars = 2 * kMaxStages + 9;         // full, empty; tfull[2], tempty[2]; done; xchg[4]
+constexpr int kNumBars = 4 * kMaxStages + 9;         // full, empty (kWgrad: landed, cleared); tfull[2], tempty[2];
+                                                     // done; xchg[4]
 constexpr int kTailHolder = kNumBars * 8;
 constexpr int kTailAbort = kTailHolder + 4;
 constexpr int kTailScan = kTailAbort + 4;            // warps' sums of the block scan
@@ -74,13 +75,14 @@ constexpr int kTailBytes = kTailCum + 4 * (kMaxLocalExperts + 1) + 1024;   // + 
 
 // Stages, epilogue warps and their shared memory, by operator.  The activation
 // and its gradient take the epilogue more arithmetic and more bytes than the
-// product alone, so they get eight warps, two per 32 lanes, for a stage less.
+// product alone, and the weights' gradient has short sums for a whole output
+// tile: they get eight warps, two per 32 lanes, for a stage less.
 template <ExpertOp kOp>
 struct Cfg {
   static constexpr bool kAct = kOp == kFwdSwiglu || kOp == kDgradSwiglu;
-  static constexpr int kStages = kOp == kWgrad ? 4 : kAct ? 5 : 6;
-  static constexpr int kStage = kOp == kWgrad ? 48 * 1024 : 32 * 1024;
-  static constexpr int kEpiWarps = kAct ? 8 : 4;
+  static constexpr int kStages = kAct || kOp == kWgrad ? 5 : 6;
+  static constexpr int kStage = 32 * 1024;
+  static constexpr int kEpiWarps = kAct || kOp == kWgrad ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kTiles = 3;                       // store tiles of an epilogue warp
   static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 2 * 1024 : kTiles * kStgTile;
@@ -246,6 +248,15 @@ __device__ __forceinline__ float2 pair_up(float a, float b, bool odd) {
   return odd ? make_float2(x, b) : make_float2(a, x);
 }
 
+// After an aborted pair: copies may still be on their way into this CTA's shared
+// memory, and complete on the other CTA's barrier, so they cannot be waited
+// for; they are left ample time.
+__device__ __noinline__ void leave_copies_time() {
+  const uint64_t now = globaltimer_ns();
+  while (globaltimer_ns() - now < 2000000ull) {
+  }
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // g and u of chunk c of a tile, arranged as pair_up leaves dh: word i of an even
@@ -353,54 +364,52 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int64_t t = t0; t < n_tiles && ok; t += t_step) {
-        const RowsTile tl = rows_tile(g, s_cum, t);
-        const uint32_t bytes = kRowsA + (kRowsB >> tl.box);
-        const int tok = static_cast<int>(tl.row0) + static_cast<int>(rank) * (tl.n / 2);
-        const int f = tl.ft * kFeatures + static_cast<int>(rank) * (kFeatures / 2);
-        for (int kb = 0; kb < g.k_blocks; ++kb) {
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          uint8_t* a = smem + stage * (kRowsA + kRowsB);
-          uint8_t* b = a + kRowsA;
-          const uint32_t bar = mapa(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
-          const int k = kb * kBlockK;
-          if constexpr (kOp == kFwd) {
-            tma_load_3d_pair(a, &maps.w, bar, k, f, tl.expert);
-          } else if constexpr (kOp == kFwdSwiglu) {
-            tma_load_3d_pair(a, &maps.w, bar, k, f, tl.expert);
-            tma_load_3d_pair(a + kRowsA / 2, &maps.w, bar, k, static_cast<int>(g.n_cols) + f, tl.expert);
-          } else {
-            tma_load_3d_pair(a, &maps.w, bar, f, k, tl.expert);
-            tma_load_3d_pair(a + kBoxBytes, &maps.w, bar, f + 64, k, tl.expert);
-          }
-          tma_load_3d_pair(b, &maps.x[tl.box], bar, k, tok, 0);
-          if (++stage == kRowsStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+    const int k_blocks = g.k_blocks;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < n_tiles && ok; t += t_step) {
+      const RowsTile tl = rows_tile(g, s_cum, t);
+      const uint32_t bytes = kRowsA + (kRowsB >> tl.box);
+      const CUtensorMap* map_x = &maps.x[tl.box];
+      const int tok = static_cast<int>(tl.row0) + static_cast<int>(rank) * (tl.n / 2);
+      const int f = tl.ft * kFeatures + static_cast<int>(rank) * (kFeatures / 2);
+      for (int kb = 0; kb < k_blocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns));
+        if (!ok) break;
+        uint8_t* a = smem + stage * (kRowsA + kRowsB);
+        uint8_t* b = a + kRowsA;
+        const uint32_t bar = mapa(smem_u32(&full[stage]), 0);
+        if (rank == 0) mbar_arrive_expect_tx_elect(&full[stage], 2 * bytes);
+        const int k = kb * kBlockK;
+        if constexpr (kOp == kFwd) {
+          tma_load_3d_pair(a, &maps.w, bar, k, f, tl.expert);
+        } else if constexpr (kOp == kFwdSwiglu) {
+          tma_load_3d_pair(a, &maps.w, bar, k, f, tl.expert);
+          tma_load_3d_pair(a + kRowsA / 2, &maps.w, bar, k, static_cast<int>(g.n_cols) + f, tl.expert);
+        } else {
+          tma_load_3d_pair(a, &maps.w, bar, f, k, tl.expert);
+          tma_load_3d_pair(a + kBoxBytes, &maps.w, bar, f + 64, k, tl.expert);
         }
-      }
-      if (!ok) {
-        set_status(g.status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
-        // copies may still be on their way into this CTA's shared memory, and
-        // complete on the other CTA's barrier: leave them ample time
-        const uint64_t now = globaltimer_ns();
-        while (globaltimer_ns() - now < 2000000ull) {
+        tma_load_3d_pair(b, map_x, bar, k, tok, 0);
+        if (++stage == kRowsStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
     }
+    if (!ok) {
+      if (lane == 0) {
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      leave_copies_time();
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0) {
+    // (values broadcast from lane 0 are known to be uniform: the MMAs' operands
+    // and the loops around them stay in uniform registers)
+    if (__shfl_sync(0xFFFFFFFFu, rank, 0) == 0) {
       constexpr bool kAMn = kOp == kDgrad || kOp == kDgradSwiglu;
       const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
@@ -625,59 +634,79 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
 // ---------------------------------------------------------------------------
 // Gradient of the weights
 // ---------------------------------------------------------------------------
-constexpr int kTileM = 128;
-constexpr int kTileN = 256;
-constexpr int kABytes = kTileM * kBlockK * 2;        // 16 KB
-constexpr int kBBytes = kTileN * kBlockK * 2;        // 32 KB
-static_assert(kABytes + kBBytes == Cfg<kWgrad>::kStage, "stage");
+constexpr int kTileM = 256;                          // dW rows of a pair's tile, 128 per CTA
+constexpr int kTileN = 256;                          // dW columns at most
 
+// This CTA pair's tiles, in turn: tile i of expert e.
 struct WgradTile {
-  int expert;
+  int expert, i;
   int64_t row0;   // the expert's first sorted row
   int mt, nt;     // output row and column tile
+  int n;          // columns of the MMA: those there are, rounded up to 32
   int kb;         // reduction blocks
   int tail;       // rows of the last one
-};
 
-__device__ __forceinline__ WgradTile wgrad_tile(const ExpertArgs& g, int64_t t) {
-  WgradTile r;
-  const int64_t per = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
-  r.expert = static_cast<int>(t / per);
-  const int64_t i = t - r.expert * per;
-  r.mt = static_cast<int>(i / g.n_tiles);
-  r.nt = static_cast<int>(i - static_cast<int64_t>(r.mt) * g.n_tiles);
-  const int n = expert_rows(g, r.expert);
-  r.row0 = g.start[r.expert];
-  r.kb = (n + kBlockK - 1) / kBlockK;
-  r.tail = n - (r.kb - 1) * kBlockK;
-  return r;
-}
+  // The pair's first tile, and the one `step` tiles on; false past the last expert.
+  __device__ __forceinline__ bool first(const ExpertArgs& g, int t) {
+    const int per = g.m_tiles * g.n_tiles;
+    expert = t / per;
+    i = t - expert * per;
+    return fill(g);
+  }
+  __device__ __forceinline__ bool next(const ExpertArgs& g, int step) {
+    const int per = g.m_tiles * g.n_tiles;
+    i += step;
+    while (i >= per) {
+      i -= per;
+      ++expert;
+    }
+    return fill(g);
+  }
+  __device__ __forceinline__ bool fill(const ExpertArgs& g) {
+    if (expert >= g.E) return false;
+    mt = i / g.n_tiles;
+    nt = i - mt * g.n_tiles;
+    const int64_t cols = g.n_cols - static_cast<int64_t>(nt) * kTileN;
+    n = cols >= kTileN ? kTileN : (static_cast<int>(cols) + 31) & ~31;
+    const int rows = expert_rows(g, expert);
+    row0 = g.start[expert];
+    kb = (rows + kBlockK - 1) / kBlockK;
+    tail = rows - (kb - 1) * kBlockK;
+    return true;
+  }
+};
 
 __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ CUtensorMap map_out, const ExpertArgs g) {
   using F = Cfg<kWgrad>;
   constexpr int kStages = F::kStages, kEpiWarps = F::kEpiWarps;
+  constexpr int kHalf = F::kStage / 2;   // a stage: 64 rows x 128 columns of dy, then of x
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kOffTail);
   uint64_t* empty = full + kStages;
-  uint64_t* tfull = full + 2 * kStages;
+  uint64_t* landed = empty + kStages;    // an expert's last rows: this CTA's copies
+  uint64_t* cleared = landed + kStages;  // ... and (the even CTA's) both CTAs' clearing
+  uint64_t* tfull = cleared + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + F::kOffTail + kTailHolder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + F::kOffTail + kTailAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&landed[s], 1);
+      mbar_init(&cleared[s], 2);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 32 * kEpiWarps);
+      mbar_init(&tempty[a], 2 * kEpiWarps);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -687,139 +716,167 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     prefetch_tensormap(&map_out);
   }
   if (warp == 1) {
-    tmem_alloc(holder, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(holder, kTmemCols);
+    tmem_relinquish_pair();
   }
   pdl_wait();
   pdl_trigger();
   report_experts(g);
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  const int64_t n_tiles = static_cast<int64_t>(g.E) * g.m_tiles * g.n_tiles;
+  const int t0 = blockIdx.x >> 1, t_step = gridDim.x >> 1;
+  WgradTile tl;
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-        const WgradTile tl = wgrad_tile(g, t);
-        for (int kb = 0; kb < tl.kb; ++kb) {
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          uint8_t* a = smem + stage * (kABytes + kBBytes);
-          uint8_t* b = a + kABytes;
-          uint64_t* bar = &full[stage];
-          mbar_arrive_expect_tx(bar, kABytes + kBBytes);
-          const int k = kb * kBlockK;
-          const int row = static_cast<int>(tl.row0) + k;
-#pragma unroll
-          for (int i = 0; i < kTileM / 64; ++i)
-            tma_load_3d(a + i * kBoxBytes, &map_a, bar, tl.mt * kTileM + 64 * i, row, 0);
-#pragma unroll
-          for (int i = 0; i < kTileN / 64; ++i)
-            tma_load_3d(b + i * kBoxBytes, &map_b, bar, tl.nt * kTileN + 64 * i, row, 0);
-          issued_mask |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
-      if (!ok) {
-        set_status(g.status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      // never leave the CTA with copies still landing in its shared memory
-      for (int s = 0; s < kStages; ++s)
-        if (issued_mask & (1u << s)) {
-          const int never = 0;
-          mbar_wait_bounded(&full[s], (issued_parity >> s) & 1u, &never, g.timeout_ns);
-        }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc = kIdesc | kAMnMajor | kBMnMajor | idesc_mn(kTileM, kTileN);
-    int stage = 0, iter = 0;
+    // ------------------------------------------------------------------ producer (both CTAs)
+    int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-      const WgradTile tl = wgrad_tile(g, t);
-      if (tl.kb == 0) continue;
-      const int acc = iter & 1;
-      ok = __all_sync(0xFFFFFFFFu,
-                      mbar_wait_bounded(&tempty[acc], ((iter >> 1) & 1) ^ 1, abort_flag, g.timeout_ns));
-      if (!ok) break;
-      ++iter;
-      tc_fence_after();
-      const uint32_t d = tmem + static_cast<uint32_t>(acc * kTileN);
+    for (bool more = tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
+      const int a0 = tl.mt * kTileM + static_cast<int>(rank) * 128;
+      const int b0 = tl.nt * kTileN + static_cast<int>(rank) * (tl.n / 2);
+      const bool two = tl.n > 128;   // boxes of 64 columns for this CTA's half of x
+      const uint32_t bytes = (two ? 4 : 3) * kBoxBytes;
       for (int kb = 0; kb < tl.kb; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns));
         if (!ok) break;
-        uint8_t* a = smem + stage * (kABytes + kBBytes);
-        uint8_t* b = a + kABytes;
-        int steps = kBlockK / 16;
+        uint8_t* a = smem + stage * F::kStage;
+        uint8_t* b = a + kHalf;
+        uint32_t bar = mapa(smem_u32(&full[stage]), 0);
         if (kb == tl.kb - 1 && tl.tail < kBlockK) {
-          // the expert's last rows: whole steps of 16 rows past its end are
-          // left out, the rest of the last step is cleared in both operands
-          // (they are consecutive in shared memory as 2 + 4 boxes of
-          // 128-byte rows; a row stays in its place under the swizzle)
-          steps = (tl.tail + 15) / 16;
-          const int clear = steps * 16 - tl.tail;
-          for (int i = lane; i < clear * 8 * 6; i += 32) {
-            const int box = i / (clear * 8), j = i - box * clear * 8;
-            uint8_t* base = box < 2 ? a + box * kBoxBytes : b + (box - 2) * kBoxBytes;
-            *reinterpret_cast<uint4*>(base + tl.tail * 128 + j * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+          // rows past the expert's are cleared by this CTA's warp 1 once its
+          // copies have landed; the stage's own barrier only keeps step
+          bar = smem_u32(&landed[stage]);
+          mbar_arrive_expect_tx_elect(&landed[stage], bytes);
+          if (rank == 0) mbar_arrive_expect_tx_elect(&full[stage], 0);
+        } else if (rank == 0) {
+          mbar_arrive_expect_tx_elect(&full[stage], 2 * bytes);
         }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t ad = smem_desc(smem_u32(a), kBoxBytes, 1024, kSwizzle128B);
-          const uint64_t bd = smem_desc(smem_u32(b), kBoxBytes, 1024, kSwizzle128B);
-          // 16 reduction rows on: 16 rows of 128 bytes down the boxes
-          for (int k = 0; k < steps; ++k)
-            mma_bf16(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(kb == 0 && k == 0));
-          tc_commit(&empty[stage]);
-          if (kb == tl.kb - 1) tc_commit(&tfull[acc]);
-        }
-        __syncwarp();
+        const int row = static_cast<int>(tl.row0) + kb * kBlockK;
+        tma_load_3d_pair(a, &map_a, bar, a0, row, 0);
+        tma_load_3d_pair(a + kBoxBytes, &map_a, bar, a0 + 64, row, 0);
+        tma_load_3d_pair(b, &map_b, bar, b0, row, 0);
+        if (two) tma_load_3d_pair(b + kBoxBytes, &map_b, bar, b0 + 64, row, 0);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
+    if (!ok) {
+      if (lane == 0) {
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      leave_copies_time();
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (even CTA); both clear
+    // (values broadcast from lane 0 are known to be uniform: the MMAs' operands
+    // and the loops around them stay in uniform registers)
+    const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const bool issues = __shfl_sync(0xFFFFFFFFu, rank, 0) == 0;
+    int stage = 0, iter = 0;
+    uint32_t phase = 0, tails = 0;   // tails: parity of each stage's clearings
+    bool ok = true;
+    // `steps` MMAs of 16 reduction rows on a stage (16 rows of 128 bytes down the boxes)
+    auto multiply = [&](uint32_t d, uint32_t idesc, bool fresh, int steps) {
+      tc_fence_after();
+      const uint32_t a = base + stage * F::kStage;
+      const uint64_t ad = smem_desc(a, kBoxBytes, 1024, kSwizzle128B);
+      const uint64_t bd = smem_desc(a + kHalf, kBoxBytes, 1024, kSwizzle128B);
+      if (steps == 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_pair(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(fresh && k == 0));
+      } else {
+        for (int k = 0; k < steps; ++k)
+          mma_bf16_pair(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(fresh && k == 0));
+      }
+      tc_commit_pair(&empty[stage]);
+    };
+    auto advance = [&]() {
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    };
+    for (bool more = tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
+      const int blocks = __shfl_sync(0xFFFFFFFFu, tl.kb, 0), tail = __shfl_sync(0xFFFFFFFFu, tl.tail, 0);
+      if (blocks == 0) continue;
+      const uint32_t idesc = kIdesc | kAMnMajor | kBMnMajor | idesc_mn(kTileM, __shfl_sync(0xFFFFFFFFu, tl.n, 0));
+      const int acc = iter & 1;
+      const uint32_t d = tm + static_cast<uint32_t>(acc * kTileN);
+      if (issues) {
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait_cluster_bounded(&tempty[acc], ((iter >> 1) & 1) ^ 1, abort_flag, g.timeout_ns));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      ++iter;
+      const int whole = tail < kBlockK ? blocks - 1 : blocks;
+      for (int kb = 0; kb < whole; ++kb) {
+        if (issues) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns));
+          if (!ok) break;
+          multiply(d, idesc, kb == 0, 4);
+        }
+        advance();
+      }
+      if (!ok) break;
+      if (whole < blocks) {
+        // the expert's last rows: whole steps of 16 past its end are left out,
+        // the rest of the last step is cleared in all four boxes (a row is 128
+        // consecutive bytes of its box, and stays in its place under the swizzle)
+        const uint32_t parity = (tails >> stage) & 1u;
+        tails ^= 1u << stage;
+        const int steps = (tail + 15) / 16;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&landed[stage], parity, abort_flag, g.timeout_ns));
+        if (!ok) break;
+        const int clear = (steps * 16 - tail) * 8;   // 16-byte pieces of a box
+        uint8_t* first = smem + stage * F::kStage + tail * 128;
+#pragma unroll
+        for (int box = 0; box < 4; ++box)
+          for (int i = lane; i < clear; i += 32)
+            *reinterpret_cast<uint4*>(first + box * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&cleared[stage]), 0));
+        __syncwarp();
+        if (issues) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns)) &&
+               __all_sync(0xFFFFFFFFu,
+                          mbar_wait_cluster_bounded(&cleared[stage], parity, abort_flag, g.timeout_ns));
+          if (!ok) break;
+          multiply(d, idesc, whole == 0, steps);
+        }
+        advance();
+      }
+      if (issues) tc_commit_pair(&tfull[acc]);
+    }
     if (!ok && lane == 0) {
       set_status(g.status, MOE_ERR_TIMEOUT);
       *abort_flag = 1;
     }
-    if (lane == 0) {
-      // all issued tensor-core work finished before the TMEM is released
-      tc_commit(done);
+    if (rank == 0) {
+      // all issued tensor-core work finished before the tensor memory is released
+      tc_commit_pair(done);
       const int never = 0;
       mbar_wait_bounded(done, 0, &never, g.timeout_ns);
     }
-    __syncwarp();
   } else {
-    // ------------------------------------------------------------------ epilogue
-    const int quad = warp & 3;
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = smem + F::kOffStg + (warp - 2) * F::kStgBytes;
     int iter = 0;
     uint32_t slot = 0;
-    for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-      const WgradTile tl = wgrad_tile(g, t);
+    for (bool more = tl.first(g, t0); more; more = tl.next(g, t_step)) {
       const int acc = iter & 1;
       if (tl.kb > 0) {
-        const bool got = mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns);
-        if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns))) {
           set_status(g.status, MOE_ERR_TIMEOUT);
           *abort_flag = 1;
           break;
@@ -828,86 +885,88 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         ++iter;
       }
       const uint32_t taddr = tmem + static_cast<uint32_t>(acc * kTileN) + (static_cast<uint32_t>(quad * 32) << 16);
-      {
-        const int64_t r0 = static_cast<int64_t>(tl.mt) * kTileM + quad * 32;
-        const int64_t col0 = static_cast<int64_t>(tl.nt) * kTileN;
+      const int64_t r0 = static_cast<int64_t>(tl.mt) * kTileM + rank * 128 + quad * 32;
+      const int64_t col0 = static_cast<int64_t>(tl.nt) * kTileN;
+      const int chunks = tl.n / 32;
+      if (tl.kb > 0 && half >= chunks) {   // nothing here for this warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+      }
 #pragma unroll 1
-        for (int c = 0; c < kTileN / 32; ++c) {
-          float f[32];
-          if (tl.kb > 0) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(taddr + c * 32, v);
-            tmem_ld_wait();
-            if (c == kTileN / 32 - 1) {
-              tc_fence_before();
-              mbar_arrive(&tempty[acc]);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+      for (int c = half; c < chunks; c += kEpiWarps / 4) {
+        float f[32];
+        if (tl.kb > 0) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + c * 32, v);
+          tmem_ld_wait();
+          if (c + kEpiWarps / 4 >= chunks) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
           }
-          if (r0 >= g.n_rows || col0 + c * 32 >= g.n_cols) continue;   // warp-uniform
-          uint4 o[4];
-          pack32(f, o);
-          if (lane == 0) bulk_wait_read<2>();   // the store from this tile three chunks ago has read it
-          __syncwarp();
-          uint8_t* tile = stg + slot * kStgTile;
-          stage_row(tile, lane, o);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            // (rows past N and columns past C are clipped by the map)
-            tma_store_3d(&map_out, tile, static_cast<int>(col0) + c * 32, static_cast<int>(r0), tl.expert);
-            bulk_commit_group();
-          }
-          slot = slot == F::kTiles - 1 ? 0 : slot + 1;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+        }
+        if (r0 >= g.n_rows) continue;        // warp-uniform
+        uint4 o[4];
+        pack32(f, o);
+        if (lane == 0) bulk_wait_read<F::kTiles - 1>();   // the store from this tile three chunks ago has read it
+        __syncwarp();
+        uint8_t* tile = stg + slot * kStgTile;
+        slot = slot == F::kTiles - 1 ? 0 : slot + 1;
+        stage_row(tile, lane, o);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          // (rows past N and columns past C are clipped by the map)
+          tma_store_3d(&map_out, tile, static_cast<int>(col0) + c * 32, static_cast<int>(r0), tl.expert);
+          bulk_commit_group();
         }
       }
     }
     if (lane == 0) bulk_wait_all();   // this warp's stores have completed
   }
-  __syncthreads();
+  // neither CTA leaves while the other's copies, MMAs or arrivals may reach it
+  __syncwarp();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
-int num_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
+// CTA pairs of a kernel that fit on the device at once.
+template <typename Kernel>
+cudaError_t resident_pairs(Kernel kernel, int threads, int smem, int* pairs) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  e = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  return *pairs < 1 ? cudaErrorInvalidConfiguration : cudaSuccess;
 }
 
 // max_tiles: at least the tiles of any split of the rows among the experts.
 template <ExpertOp kOp>
 cudaError_t launch_rows(const RowsMaps& maps, const ExpertArgs& g, int64_t max_tiles, cudaStream_t s) {
-  static int pairs = 0;   // CTA pairs that fit on the device at once
   using F = Cfg<kOp>;
-  if (pairs == 0) {
-    cudaError_t e =
-        cudaFuncSetAttribute(expert_rows_kernel<kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+  static int pairs = 0;
+  if (pairs < 1) {
+    const cudaError_t e = resident_pairs(expert_rows_kernel<kOp>, F::kThreads, F::kSmem, &pairs);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(F::kThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, expert_rows_kernel<kOp>, &cfg);
-    if (e != cudaSuccess) return e;
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
-    pairs = clusters;
   }
   const int grid = 2 * static_cast<int>(max_tiles < pairs ? max_tiles : pairs);
   return launch_pdl_cluster(expert_rows_kernel<kOp>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, maps, g);
@@ -915,17 +974,14 @@ cudaError_t launch_rows(const RowsMaps& maps, const ExpertArgs& g, int64_t max_t
 
 cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const ExpertArgs& g,
                          int64_t tiles, cudaStream_t s) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(expert_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kWgrad>::kSmem);
+  using F = Cfg<kWgrad>;
+  static int pairs = 0;
+  if (pairs < 1) {
+    const cudaError_t e = resident_pairs(expert_wgrad_kernel, F::kThreads, F::kSmem, &pairs);
     if (e != cudaSuccess) return e;
-    attr_set = true;
   }
-  const int sms = num_sms();
-  if (sms < 1) return cudaErrorInvalidDevice;
-  return launch_pdl(expert_wgrad_kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(Cfg<kWgrad>::kThreads),
-                    Cfg<kWgrad>::kSmem, s, a, b, out, g);
+  const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+  return launch_pdl_cluster(expert_wgrad_kernel, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, a, b, out, g);
 }
 
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
