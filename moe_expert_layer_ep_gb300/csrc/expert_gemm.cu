@@ -85,7 +85,7 @@ struct Cfg {
   static constexpr int kEpiWarps = kAct || kOp == kWgrad ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kTiles = 3;                       // store tiles of an epilogue warp
-  static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 2 * 1024 : kTiles * kStgTile;
+  static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 2 * 1024 : kOp == kWgrad ? 4096 : kTiles * kStgTile;
   static constexpr int kOffStg = kStages * kStage;
   static constexpr int kOffTail = kOffStg + kEpiWarps * kStgBytes;
   static constexpr int kSmem = kOffTail + kTailBytes;
@@ -138,18 +138,12 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
 }
 
-__device__ __forceinline__ void pack32(const float (&f)[32], uint4 (&o)[4]) {
-#pragma unroll
-  for (int v = 0; v < 4; ++v)
-    o[v] = make_uint4(pack_bf16x2(f[8 * v], f[8 * v + 1]), pack_bf16x2(f[8 * v + 2], f[8 * v + 3]),
-                      pack_bf16x2(f[8 * v + 4], f[8 * v + 5]), pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
-}
-
-// This lane's 32 columns of its row into a store tile (64-byte rows, 64-byte
-// swizzle: 16-byte piece j of row r at r * 64 + ((j ^ ((r >> 1) & 3)) * 16)).
-__device__ __forceinline__ void stage_row(uint8_t* tile, int lane, const uint4 (&o)[4]) {
-#pragma unroll
-  for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(tile + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) = o[v];
+// Eight accumulator values as bf16.
+__device__ __forceinline__ uint4 pack8(const uint32_t* v) {
+  return make_uint4(pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                    pack_bf16x2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                    pack_bf16x2(__uint_as_float(v[4]), __uint_as_float(v[5])),
+                    pack_bf16x2(__uint_as_float(v[6]), __uint_as_float(v[7])));
 }
 
 // Two features of a token into a store tile: 64-byte rows, 64-byte swizzle.
@@ -505,7 +499,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       const uint32_t taddr = tmem + static_cast<uint32_t>(acc * kTokens) + (static_cast<uint32_t>(quad * 32) << 16);
       if (half >= chunks) {   // nothing here for this warp
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
       }
       for (int c = half; c < chunks; c += kStep) {
         const int tok = c * 32;
@@ -519,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
         if (c + kStep >= chunks) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+          if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
         }
         if (left <= 0) continue;   // warp-uniform
         if constexpr (kOp == kFwd || kOp == kDgrad) {
@@ -842,9 +836,11 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         for (int box = 0; box < 4; ++box)
           for (int i = lane; i < clear; i += 32)
             *reinterpret_cast<uint4*>(first + box * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+        // (each SM's tensor core reads its own CTA's shared memory: the stores
+        // are ordered before that by this fence, in this CTA)
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&cleared[stage]), 0));
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&cleared[stage]), 0));
         __syncwarp();
         if (issues) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns)) &&
@@ -869,13 +865,20 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue (both CTAs)
+    // 64 columns at a time (every other 64 of the tile): two tensor-memory
+    // loads, one 32-row x 128-byte store tile (128-byte swizzle: 16-byte piece
+    // j of row r at r * 128 + ((j ^ (r & 7)) * 16)), one store of whole lines
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* stg = smem + F::kOffStg + (warp - 2) * F::kStgBytes;
+    uint8_t* tile = smem + F::kOffStg + (warp - 2) * F::kStgBytes;
     int iter = 0;
-    uint32_t slot = 0;
-    for (bool more = tl.first(g, t0); more; more = tl.next(g, t_step)) {
-      const int acc = iter & 1;
-      if (tl.kb > 0) {
+    bool more = tl.first(g, t0);
+    while (more) {
+      const int acc = iter & 1, n = tl.n, expert = tl.expert;
+      const bool any = tl.kb > 0;
+      const int64_t r0 = static_cast<int64_t>(tl.mt) * kTileM + rank * 128 + quad * 32;
+      const int64_t col0 = static_cast<int64_t>(tl.nt) * kTileN;
+      more = tl.next(g, t_step);   // (its loads are on their way while this tile is waited for)
+      if (any) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns))) {
           set_status(g.status, MOE_ERR_TIMEOUT);
           *abort_flag = 1;
@@ -885,44 +888,44 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         ++iter;
       }
       const uint32_t taddr = tmem + static_cast<uint32_t>(acc * kTileN) + (static_cast<uint32_t>(quad * 32) << 16);
-      const int64_t r0 = static_cast<int64_t>(tl.mt) * kTileM + rank * 128 + quad * 32;
-      const int64_t col0 = static_cast<int64_t>(tl.nt) * kTileN;
-      const int chunks = tl.n / 32;
-      if (tl.kb > 0 && half >= chunks) {   // nothing here for this warp
+      if (any && 64 * half >= n) {   // nothing here for this warp
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
       }
 #pragma unroll 1
-      for (int c = half; c < chunks; c += kEpiWarps / 4) {
-        float f[32];
-        if (tl.kb > 0) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(taddr + c * 32, v);
+      for (int c = 64 * half; c < n; c += 64 * (kEpiWarps / 4)) {
+        uint4 o[8];
+        if (any) {
+          // (the second 32 columns may lie past the MMA's: loaded all the same,
+          // from columns of this accumulator, and clipped by the store)
+          uint32_t v[32], u[32];
+          tmem_ld_32x32b_x32(taddr + c, v);
+          tmem_ld_32x32b_x32(taddr + c + 32, u);
           tmem_ld_wait();
-          if (c + kEpiWarps / 4 >= chunks) {
+          if (c + 64 * (kEpiWarps / 4) >= n) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+            if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+          for (int j = 0; j < 4; ++j) {
+            o[j] = pack8(v + 8 * j);
+            o[4 + j] = pack8(u + 8 * j);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = 0.0f;
+          for (int j = 0; j < 8; ++j) o[j] = make_uint4(0, 0, 0, 0);
         }
         if (r0 >= g.n_rows) continue;        // warp-uniform
-        uint4 o[4];
-        pack32(f, o);
-        if (lane == 0) bulk_wait_read<F::kTiles - 1>();   // the store from this tile three chunks ago has read it
+        if (lane == 0) bulk_wait_read<0>();  // the store before has read the tile
         __syncwarp();
-        uint8_t* tile = stg + slot * kStgTile;
-        slot = slot == F::kTiles - 1 ? 0 : slot + 1;
-        stage_row(tile, lane, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(tile + lane * 128 + ((j ^ (lane & 7)) << 4)) = o[j];
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           // (rows past N and columns past C are clipped by the map)
-          tma_store_3d(&map_out, tile, static_cast<int>(col0) + c * 32, static_cast<int>(r0), tl.expert);
+          tma_store_3d(&map_out, tile, static_cast<int>(col0) + c, static_cast<int>(r0), expert);
           bulk_commit_group();
         }
       }
@@ -1183,8 +1186,8 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
   if ((st = rows_map(&b, x, rows, C, x_ld, kBlockK)) != MOE_OK) return st;
   const uint64_t d[3] = {static_cast<uint64_t>(C), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
   const uint64_t strides[2] = {static_cast<uint64_t>(C) * 2, static_cast<uint64_t>(N) * static_cast<uint64_t>(C) * 2};
-  const uint32_t box[3] = {32, 32, 1};
-  if ((st = encode_tiled_map(&o, dw, kBf16, 3, d, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) != MOE_OK) return st;
+  const uint32_t box[3] = {64, 32, 1};
+  if ((st = encode_tiled_map(&o, dw, kBf16, 3, d, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) != MOE_OK) return st;
   ExpertArgs g = expert_args(rows, E, start, counts, status);
   g.n_tiles = ceil_div(C, kTileN);
   g.m_tiles = ceil_div(N, kTileM);
