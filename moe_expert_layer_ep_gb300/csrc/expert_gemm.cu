@@ -71,16 +71,15 @@ constexpr int kTailHolder = kNumBars * 8;
 constexpr int kTailAbort = kTailHolder + 4;
 constexpr int kTailScan = kTailAbort + 4;            // warps' sums of the block scan
 constexpr int kTailCum = kTailScan + 64;             // token blocks of the experts before e, [E + 1]
-constexpr int kTailBytes = kTailCum + 4 * (kMaxLocalExperts + 1) + 1024;   // + alignment slack
 
 // Stages, epilogue warps and their shared memory, by operator.  The activation
 // and its gradient take the epilogue more arithmetic and more bytes than the
 // product alone, and the weights' gradient has short sums for a whole output
-// tile: they get eight warps, two per 32 lanes, for a stage less.
+// tile: they get eight warps, two per 32 lanes, the former for a stage less.
 template <ExpertOp kOp>
 struct Cfg {
   static constexpr bool kAct = kOp == kFwdSwiglu || kOp == kDgradSwiglu;
-  static constexpr int kStages = kAct || kOp == kWgrad ? 5 : 6;
+  static constexpr int kStages = kAct ? 5 : 6;
   static constexpr int kStage = 32 * 1024;
   static constexpr int kEpiWarps = kAct || kOp == kWgrad ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -88,7 +87,7 @@ struct Cfg {
   static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 2 * 1024 : kOp == kWgrad ? 4096 : kTiles * kStgTile;
   static constexpr int kOffStg = kStages * kStage;
   static constexpr int kOffTail = kOffStg + kEpiWarps * kStgBytes;
-  static constexpr int kSmem = kOffTail + kTailBytes;
+  static constexpr int kSmem = kOffTail + kTailCum + (kOp == kWgrad ? 0 : 4 * (kMaxLocalExperts + 1)) + 1024;   // + slack
   static_assert(kSmem <= 227 * 1024 && kStages <= kMaxStages && kEpiWarps <= kMaxEpiWarps, "shared memory");
 };
 
