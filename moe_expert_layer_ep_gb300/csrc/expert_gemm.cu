@@ -204,7 +204,7 @@ struct RowsTile {
   int64_t row0;   // first sorted row
   int valid;      // tokens
   int n;          // tokens of the MMA: valid rounded up to 32
-  int box;        // the map of x that loads half of them: 128 >> box rows
+  int box;        // the map of x that loads half of them: 128 - 32 * box rows
   int ft;         // feature tile
 };
 
@@ -229,7 +229,7 @@ __device__ __forceinline__ RowsTile rows_tile(const ExpertArgs& g, const int32_t
   const int left = count - b * tall;
   r.valid = left < tall ? left : tall;
   r.n = (r.valid + 31) & ~31;
-  r.box = r.n > 128 ? 0 : r.n > 64 ? 1 : 2;
+  r.box = (256 - r.n) / 64;
   return r;
 }
 
@@ -269,13 +269,13 @@ __device__ __forceinline__ void load_gate_up(const ExpertArgs& g, const RowsTile
   }
 }
 
-// Tensor maps of a rows launch.  x: the tokens in boxes of 128, 64 and 32 rows (a
+// Tensor maps of a rows launch.  x: the tokens in boxes of 128, 96, 64, 32 rows (a
 // tile takes the smallest that holds its half of the tokens: one copy per stage,
 // as more copies of fewer bytes are slower: 358 us in 32-row boxes, 300 us so,
 // at 16384 x 4096 x 4096); out: the output or its first half, out2: its second
 // half, h: kFwdSwiglu's third output.
 struct RowsMaps {
-  CUtensorMap w, x[3], out, out2, h;
+  CUtensorMap w, x[4], out, out2, h;
 };
 
 template <ExpertOp kOp>
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     bool ok = true;
     for (int64_t t = t0; t < n_tiles && ok; t += t_step) {
       const RowsTile tl = rows_tile(g, s_cum, t);
-      const uint32_t bytes = kRowsA + (kRowsB >> tl.box);
+      const uint32_t bytes = kRowsA + kRowsB / 4 * (4 - tl.box);
       const CUtensorMap* map_x = &maps.x[tl.box];
       const int tok = static_cast<int>(tl.row0) + static_cast<int>(rank) * (tl.n / 2);
       const int f = tl.ft * kFeatures + static_cast<int>(rank) * (kFeatures / 2);
@@ -1002,10 +1002,10 @@ moe_status_t weights_map(CUtensorMap* m, const void* p, int64_t E, int64_t n, in
   const uint32_t box[3] = {64, box_rows, 1};
   return encode_tiled_map(m, p, kBf16, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// x of a rows launch: boxes of 128, 64 and 32 rows.
+// x of a rows launch: boxes of 128, 96, 64 and 32 rows.
 moe_status_t token_maps(RowsMaps* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
-  for (int i = 0; i < 3; ++i) {
-    const moe_status_t st = rows_map(&m->x[i], p, rows, cols, ld, 128 >> i);
+  for (int i = 0; i < 4; ++i) {
+    const moe_status_t st = rows_map(&m->x[i], p, rows, cols, ld, 128 - 32 * i);
     if (st != MOE_OK) return st;
   }
   return MOE_OK;
