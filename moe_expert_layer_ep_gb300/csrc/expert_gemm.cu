@@ -69,25 +69,27 @@ constexpr int kNumBars = 4 * kMaxStages + 9;         // full, empty (kWgrad: lan
                                                      // done; xchg[4]
 constexpr int kTailHolder = kNumBars * 8;
 constexpr int kTailAbort = kTailHolder + 4;
-constexpr int kTailScan = kTailAbort + 4;            // warps' sums of the block scan
-constexpr int kTailCum = kTailScan + 64;             // token blocks of the experts before e, [E + 1]
+constexpr int kTailCum = kTailAbort + 4;             // token blocks of the 32-expert groups before, [33]
+constexpr int kTailBytes = kTailCum + 33 * 4 + 1024;   // + alignment slack
 
 // Stages, epilogue warps and their shared memory, by operator.  The activation
 // and its gradient take the epilogue more arithmetic and more bytes than the
 // product alone, and the weights' gradient has short sums for a whole output
-// tile: they get eight warps, two per 32 lanes, the former for a stage less.
+// tile: they get eight warps, two per 32 lanes.  Six stages where they fit (the
+// activation's gradient: 343 us with five, 330 us with six and a store tile less
+// per warp, at 16384 rows x 7168 x 2048).
 template <ExpertOp kOp>
 struct Cfg {
   static constexpr bool kAct = kOp == kFwdSwiglu || kOp == kDgradSwiglu;
-  static constexpr int kStages = kAct ? 5 : 6;
+  static constexpr int kStages = kOp == kFwdSwiglu ? 5 : 6;
   static constexpr int kStage = 32 * 1024;
   static constexpr int kEpiWarps = kAct || kOp == kWgrad ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kTiles = 3;                       // store tiles of an epilogue warp
+  static constexpr int kTiles = kOp == kDgradSwiglu ? 2 : 3;   // store tiles of an epilogue warp
   static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 2 * 1024 : kOp == kWgrad ? 4096 : kTiles * kStgTile;
   static constexpr int kOffStg = kStages * kStage;
   static constexpr int kOffTail = kOffStg + kEpiWarps * kStgBytes;
-  static constexpr int kSmem = kOffTail + kTailCum + (kOp == kWgrad ? 0 : 4 * (kMaxLocalExperts + 1)) + 1024;   // + slack
+  static constexpr int kSmem = kOffTail + kTailBytes;
   static_assert(kSmem <= 227 * 1024 && kStages <= kMaxStages && kEpiWarps <= kMaxEpiWarps, "shared memory");
 };
 
@@ -208,24 +210,37 @@ struct RowsTile {
   int ft;         // feature tile
 };
 
-__device__ __forceinline__ RowsTile rows_tile(const ExpertArgs& g, const int32_t* s_cum, int64_t t) {
-  RowsTile r;
-  int lo = 0, hi = g.E - 1;   // the expert whose tiles hold t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(s_cum[mid + 1]) * g.n_tiles > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+__device__ __forceinline__ int token_blocks(int rows) { return (rows + kTokens - 1) / kTokens; }
+
+// Tile t, looked up by a whole, converged warp: the group of 32 experts that
+// holds it from the groups' sums, then the expert from the counts of the group,
+// one per lane.  The same in all lanes.
+__device__ __forceinline__ RowsTile rows_tile(const ExpertArgs& g, const int32_t* s_cum, int64_t t, int lane) {
+  constexpr unsigned kAll = 0xFFFFFFFFu;
+  const bool past = lane * 32 < g.E && static_cast<int64_t>(s_cum[lane + 1]) * g.n_tiles > t;
+  const int group = __ffs(__ballot_sync(kAll, past)) - 1;
+  const int e = group * 32 + lane;
+  const int rows = e < g.E ? expert_rows(g, e) : 0;
+  const int start = e < g.E ? g.start[e] : 0;
+  const int mine = token_blocks(rows);
+  int end = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, end, o);
+    if (lane >= o) end += y;
   }
-  const int first = s_cum[lo], blocks = s_cum[lo + 1] - first, count = g.counts[lo];
+  end += s_cum[group];
+  const int at = __ffs(__ballot_sync(kAll, static_cast<int64_t>(end) * g.n_tiles > t)) - 1;
+  const int blocks = __shfl_sync(kAll, mine, at), first = __shfl_sync(kAll, end, at) - blocks;
+  const int count = __shfl_sync(kAll, rows, at);
+  RowsTile r;
+  r.expert = group * 32 + at;
   // token blocks innermost: they share a weight tile while it is in L2
   const int i = static_cast<int>(t - static_cast<int64_t>(first) * g.n_tiles);
   r.ft = i / blocks;
   const int b = i - r.ft * blocks;
   const int tall = ((count + blocks - 1) / blocks + 31) & ~31;
-  r.expert = lo;
-  r.row0 = static_cast<int64_t>(g.start[lo]) + b * tall;
+  r.row0 = static_cast<int64_t>(__shfl_sync(kAll, start, at)) + b * tall;
   const int left = count - b * tall;
   r.valid = left < tall ? left : tall;
   r.n = (r.valid + 31) & ~31;
@@ -282,7 +297,7 @@ template <ExpertOp kOp>
 __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     expert_rows_kernel(const __grid_constant__ RowsMaps maps, const ExpertArgs g) {
   using F = Cfg<kOp>;
-  constexpr int kRowsStages = F::kStages, kEpiWarps = F::kEpiWarps, kThreads = F::kThreads;
+  constexpr int kRowsStages = F::kStages, kEpiWarps = F::kEpiWarps;
   constexpr int kFeatures = kOp == kFwdSwiglu ? 128 : 256;   // output features of a tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -295,7 +310,6 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
   uint64_t* xchg = done + 1;   // kFwdSwiglu: the warps of g and of u
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + F::kOffTail + kTailHolder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + F::kOffTail + kTailAbort);
-  int32_t* s_scan = reinterpret_cast<int32_t*>(smem + F::kOffTail + kTailScan);
   int32_t* s_cum = reinterpret_cast<int32_t*>(smem + F::kOffTail + kTailCum);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -323,28 +337,23 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  {
-    // token blocks of the experts before each: a thread takes consecutive
-    // experts, and the threads' sums are scanned
-    const int per = (g.E + kThreads - 1) / kThreads;
-    const int e0 = threadIdx.x * per;
-    int sum = 0;
-    for (int e = e0; e < e0 + per && e < g.E; ++e) sum += (expert_rows(g, e) + kTokens - 1) / kTokens;
-    int x = sum;
+  // token blocks of each group of 32 experts, one warp per group, and their sums
+  const int groups = (g.E + 31) / 32;
+  for (int k = warp; k < groups; k += F::kThreads / 32) {
+    const int e = k * 32 + lane;
+    const int blocks = __reduce_add_sync(0xFFFFFFFFu, e < g.E ? token_blocks(expert_rows(g, e)) : 0);
+    if (lane == 0) s_cum[k + 1] = blocks;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int x = lane < groups ? s_cum[lane + 1] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    int base = x - sum;
-    for (int w = 0; w < warp; ++w) base += s_scan[w];
-    for (int e = e0; e < e0 + per && e < g.E; ++e) {
-      s_cum[e] = base;
-      base += (expert_rows(g, e) + kTokens - 1) / kTokens;
-      if (e == g.E - 1) s_cum[g.E] = base;
-    }
+    s_cum[lane + 1] = x;
+    if (lane == 0) s_cum[0] = 0;
   }
   report_experts(g);
   tc_fence_before();
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  const int64_t n_tiles = static_cast<int64_t>(s_cum[g.E]) * g.n_tiles;
+  const int64_t n_tiles = static_cast<int64_t>(s_cum[32]) * g.n_tiles;
   const int64_t t0 = blockIdx.x >> 1, t_step = gridDim.x >> 1;
 
   if (warp == 0) {
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t t = t0; t < n_tiles && ok; t += t_step) {
-      const RowsTile tl = rows_tile(g, s_cum, t);
+      const RowsTile tl = rows_tile(g, s_cum, t, lane);
       const uint32_t bytes = kRowsA + kRowsB / 4 * (4 - tl.box);
       const CUtensorMap* map_x = &maps.x[tl.box];
       const int tok = static_cast<int>(tl.row0) + static_cast<int>(rank) * (tl.n / 2);
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int64_t t = t0; t < n_tiles && ok; t += t_step, ++iter) {
-        const RowsTile tl = rows_tile(g, s_cum, t);
+        const RowsTile tl = rows_tile(g, s_cum, t, lane);
         const uint32_t idesc =
             kIdesc | (kAMn ? kAMnMajor : 0u) | idesc_mn(256, __shfl_sync(0xFFFFFFFFu, tl.n, 0));
         const int acc = iter & 1;
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       return tile;
     };
     for (int64_t t = t0; t < n_tiles; t += t_step, ++iter) {
-      const RowsTile tl = rows_tile(g, s_cum, t);
+      const RowsTile tl = rows_tile(g, s_cum, t, lane);
       const int acc = iter & 1;
       // this warp's 32 features, from col (kFwdSwiglu: quads 0 and 1 hold g, 2 and 3 the same features' u)
       const int64_t col = static_cast<int64_t>(tl.ft) * kFeatures + static_cast<int>(rank) * (kFeatures / 2) +
