@@ -326,19 +326,155 @@ moe_status_t check_sort(int64_t T, int32_t topk, int64_t K, int32_t elem, int64_
   return MOE_OK;
 }
 
+// ---------------------------------------------------------------------------
+// The plan
+// ---------------------------------------------------------------------------
+// A stable counting sort of the assignments by expert in two kernels.  The
+// assignments are cut into at most kPlanParts parts of whole 512s, one CTA
+// each.  sort_count leaves each part's experts' counts and every assignment's
+// rank among its expert's within the part (warp match, per-warp counts,
+// running counts over the part's 512s); sort_place adds the counts of the parts
+// before and of the experts before.  Every CTA sums the whole count table
+// itself (128 KB at 256 experts, from L2): cheaper than a kernel between the
+// two.  Integers only; nothing depends on the order of anything.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanParts = 128;
+
+struct SortPlanArgs {
+  const int32_t* ids;
+  int64_t A;
+  int32_t E_global, E, first;
+  int32_t parts, per_part;   // 512s of a part
+  int32_t* status;
+  int32_t* hist;             // [parts][E]
+  int32_t* rank;             // [A]
+  int32_t* src2dst;
+  int32_t* start;
+  int32_t* counts;
+};
+
+// Local expert of assignment i, -1 when it has none.
+__device__ __forceinline__ int sort_expert(const SortPlanArgs& p, int64_t i, bool* bad) {
+  const int id = p.ids[i];
+  *bad = id < -1 || id >= p.E_global;
+  const int e = id - p.first;
+  return !*bad && id >= 0 && e >= 0 && e < p.E ? e : -1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) sort_count_kernel(SortPlanArgs p) {
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ uint16_t s_warp[kWarps][kMaxLocalExperts];
+  __shared__ int32_t s_run[kMaxLocalExperts];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && tid < 4) p.status[tid] = 0;   // (only the next kernel sets it)
+  for (int e = tid; e < p.E; e += kPlanThreads) s_run[e] = 0;
+  for (int r = 0; r < p.per_part; ++r) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * p.per_part + r) * kPlanThreads + tid;
+    for (int e = tid; e < p.E; e += kPlanThreads)
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s_warp[w][e] = 0;
+    bool bad;
+    const int e = i < p.A ? sort_expert(p, i, &bad) : -1;
+    __syncthreads();
+    const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
+    const int before = __popc(peers & ((1u << lane) - 1u));
+    if (e >= 0 && before == 0) s_warp[warp][e] = static_cast<uint16_t>(__popc(peers));
+    __syncthreads();
+    if (e >= 0) {
+      int rank = s_run[e] + before;
+      for (int w = 0; w < warp; ++w) rank += s_warp[w][e];
+      p.rank[i] = rank;
+    }
+    __syncthreads();
+    for (int x = tid; x < p.E; x += kPlanThreads) {
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) n += s_warp[w][x];
+      s_run[x] += n;
+    }
+    __syncthreads();
+  }
+  for (int e = tid; e < p.E; e += kPlanThreads) p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = s_run[e];
+}
+
+__global__ void __launch_bounds__(kPlanThreads) sort_place_kernel(SortPlanArgs p) {
+  __shared__ int32_t s_total[kMaxLocalExperts], s_before[kMaxLocalExperts], s_sum[kPlanThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int e = tid; e < p.E; e += kPlanThreads) s_total[e] = s_before[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  // few experts: several threads share one, taking every few parts
+  int span = 32;
+  while (span < p.E && span < kPlanThreads) span <<= 1;
+  const int step = kPlanThreads / span;
+  for (int e = tid & (span - 1); e < p.E; e += span) {
+    int total = 0, before = 0;
+#pragma unroll 8
+    for (int c = tid / span; c < p.parts; c += step) {
+      const int n = p.hist[static_cast<int64_t>(c) * p.E + e];
+      total += n;
+      if (c < blockIdx.x) before += n;
+    }
+    if (total) atomicAdd(&s_total[e], total);
+    if (before) atomicAdd(&s_before[e], before);
+  }
+  __syncthreads();
+  // experts' first rows: two consecutive experts per thread, scanned
+  const int e0 = 2 * tid;
+  const int n0 = e0 < p.E ? s_total[e0] : 0, n1 = e0 + 1 < p.E ? s_total[e0 + 1] : 0;
+  const int r0 = (n0 + kBlockM - 1) / kBlockM * kBlockM, r1 = (n1 + kBlockM - 1) / kBlockM * kBlockM;
+  int x = r0 + r1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_sum[warp] = x;
+  __syncthreads();
+  int row = x - r0 - r1;
+  for (int w = 0; w < warp; ++w) row += s_sum[w];
+  if (e0 < p.E) s_before[e0] += row;
+  if (e0 + 1 < p.E) s_before[e0 + 1] += row + r0;
+  if (blockIdx.x == 0) {
+    if (e0 < p.E) {
+      p.start[e0] = row;
+      p.counts[e0] = n0;
+    }
+    if (e0 + 1 < p.E) {
+      p.start[e0 + 1] = row + r0;
+      p.counts[e0 + 1] = n1;
+    }
+  }
+  __syncthreads();
+  for (int r = 0; r < p.per_part; ++r) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * p.per_part + r) * kPlanThreads + tid;
+    if (i >= p.A) break;
+    bool bad;
+    const int e = sort_expert(p, i, &bad);
+    if (bad) set_status(p.status, MOE_ERR_EXPERT_ID);
+    p.src2dst[i] = e >= 0 ? s_before[e] + p.rank[i] : -1;
+  }
+}
+
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
 struct SortWs {
   uint64_t meta, padded, hist, rank, total;
-  int64_t chunks;
+  int32_t parts, per_part;
 };
 SortWs sort_ws(int64_t A, int32_t E) {
   SortWs w;
-  w.chunks = (A + kPlanChunk - 1) / kPlanChunk;
+  const int64_t blocks = (A + kPlanThreads - 1) / kPlanThreads;
+  w.per_part = static_cast<int32_t>((blocks + kPlanParts - 1) / kPlanParts);
+  w.parts = w.per_part ? static_cast<int32_t>((blocks + w.per_part - 1) / w.per_part) : 1;
+  // (the one-CTA plan uses meta and padded, the two kernels hist and rank)
   w.meta = 256;   // the status word comes first
   w.padded = w.meta + 256;
   w.hist = w.padded + align256(4 * static_cast<uint64_t>(E));
-  w.rank = w.hist + align256(4 * static_cast<uint64_t>(w.chunks) * E);
+  w.rank = w.hist + align256(4 * static_cast<uint64_t>(w.parts) * E);
   w.total = w.rank + align256(4 * static_cast<uint64_t>(A));
   return w;
 }
@@ -370,23 +506,43 @@ moe_status_t moe_sort_plan(const int32_t* topk_ids, int64_t T, int32_t topk, int
   const moe::SortWs w = moe::sort_ws(A, E_local);
   if (ws_bytes < static_cast<int64_t>(w.total)) return MOE_ERR_BUFFER_TOO_SMALL;
   uint8_t* base = static_cast<uint8_t*>(ws);
-  moe::PlanArgs p;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (moe::plan_is_small(A, E_local)) {   // one CTA: 3.7 us where the two kernels take 6
+    moe::PlanArgs p;
+    memset(&p, 0, sizeof(p));
+    p.topk_ids = topk_ids;
+    p.A = A;
+    p.E_global = E_global;
+    p.E_local = E_local;
+    p.expert_start = expert_start;
+    p.status = reinterpret_cast<int32_t*>(base);
+    p.meta = reinterpret_cast<int32_t*>(base + w.meta);
+    p.counts = counts;
+    p.padded = reinterpret_cast<int32_t*>(base + w.padded);
+    p.start = start;
+    p.src2dst = src2dst;
+    return moe::launch_plan(p, cs) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  moe::SortPlanArgs p;
   memset(&p, 0, sizeof(p));
-  p.topk_ids = topk_ids;
+  p.ids = topk_ids;
   p.A = A;
   p.E_global = E_global;
-  p.E_local = E_local;
-  p.expert_start = expert_start;
-  p.chunks = static_cast<int32_t>(w.chunks);
+  p.E = E_local;
+  p.first = expert_start;
+  p.parts = w.parts;
+  p.per_part = w.per_part;
   p.status = reinterpret_cast<int32_t*>(base);
-  p.meta = reinterpret_cast<int32_t*>(base + w.meta);
-  p.counts = counts;
-  p.padded = reinterpret_cast<int32_t*>(base + w.padded);
-  p.start = start;
+  p.hist = reinterpret_cast<int32_t*>(base + w.hist);
+  p.rank = reinterpret_cast<int32_t*>(base + w.rank);
   p.src2dst = src2dst;
-  p.chunk_hist = reinterpret_cast<int32_t*>(base + w.hist);
-  p.chunk_rank = reinterpret_cast<int32_t*>(base + w.rank);
-  return moe::launch_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  p.start = start;
+  p.counts = counts;
+  const dim3 grid(static_cast<unsigned>(w.parts)), block(moe::kPlanThreads);
+  if (moe::launch_pdl(moe::sort_count_kernel, grid, block, 0, cs, p) != cudaSuccess ||
+      moe::launch_pdl(moe::sort_place_kernel, grid, block, 0, cs, p) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 moe_status_t moe_sort_tokens(const void* x, int64_t x_ld, const int32_t* src2dst, int64_t T, int32_t topk, int64_t K,

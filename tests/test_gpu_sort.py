@@ -90,6 +90,27 @@ def test_sort_and_back(case):
     assert not np.any(_f64(dw)[dst < 0])
 
 
+@pytest.mark.parametrize("T,E,El,first,k", [(0, 300, 300, 0, 2), (1, 1024, 1024, 0, 1), (256, 256, 256, 0, 8),
+                                            (257, 256, 256, 0, 8), (1024, 64, 64, 0, 3), (512, 8, 8, 0, 5), (70, 600, 257, 340, 64),
+                                            (9000, 1024, 1000, 24, 8), (30001, 64, 32, 16, 8), (66000, 4, 4, 0, 1)])
+def test_plan_of_any_size(T, E, El, first, k):
+    """Every kernel of the plan (one CTA; parts of one and of several 512s), ragged ends, a status word that a call
+    clears, scratch that held something else."""
+    ids = _ids(T, E, k, T + E, 0.05)
+    ws = torch.full((M.moe_sort_plan_workspace_size(T, k, El) + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = M.moe_sort_plan(ids.cuda(), E, El, first, ws=ws[:-256])
+    assert M.moe_read_device_status(ws) == 0
+    assert torch.all(ws[-256:] == 0xA5)
+    for a, b in zip(got, R.sort_plan(ids.numpy(), E, El, first)):
+        assert np.array_equal(a.cpu().numpy(), b)
+    if T > 4:
+        ids[3, 0], ids[T // 2, k - 1] = E, -2
+        got = M.moe_sort_plan(ids.cuda(), E, El, first, ws=ws[:-256])
+        assert M.moe_read_device_status(ws) == M.STATUS["MOE_ERR_EXPERT_ID"]
+        for a, b in zip(got, R.sort_plan(ids.numpy(), E, El, first)):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+
 def test_directional_derivative_of_the_weighted_way_back():
     """<dout, unsort(y, w)> is bilinear in y and w: its change along (v, z) is the gradients' product with them."""
     T, K, E, k = 60, 96, 8, 3
