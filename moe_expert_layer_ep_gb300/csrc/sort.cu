@@ -81,6 +81,13 @@ struct Picks {
   int32_t d[kSortThreads / 32][kMaxTopk];
   float w[kSortThreads / 32][kMaxTopk];
 };
+// All threads that share a token.
+__device__ __forceinline__ void group_sync(int slot, int lanes) {
+  if (lanes == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(lanes) : "memory");
+}
 __device__ __forceinline__ void load_picks(const SortArgs& a, Picks& s, int64_t t, int slot, int lane, int lanes) {
   if (t < a.T)
     for (int j = lane; j < a.topk; j += lanes) {
@@ -88,7 +95,7 @@ __device__ __forceinline__ void load_picks(const SortArgs& a, Picks& s, int64_t 
       s.d[slot][j] = d < a.rows ? d : -1;
       s.w[slot][j] = a.w ? a.w[t * a.topk + j] : 1.0f;
     }
-  __syncthreads();
+  group_sync(slot, lanes);
 }
 
 template <typename E, int kVec>
@@ -181,16 +188,24 @@ __global__ void __launch_bounds__(kSortThreads) unsort_tokens_kernel(SortArgs a)
   }
 }
 
-template <typename E, int kVec>
-__global__ void __launch_bounds__(kSortThreads) unsort_backward_kernel(SortArgs a) {
+// kBackJ selections' rows in flight per thread.  A token is one short chain of
+// loads, stores and a reduction, so it is other tokens on the SM that keep the
+// memory busy: a token gets no more warps than leave kBackWarps in all, and
+// rows that are read element by element, or few per token, take fewer registers
+// for more CTAs per SM.  T = 4096, K = 2048, top-8, bf16: 55 us with a CTA per
+// token, 47 us so; T = 8192, K = 1001, top-4, fp32: 121 us, 69 us.
+constexpr int64_t kBackWarps = 7000;
+
+template <typename E, int kVec, int kBackJ>
+__global__ void __launch_bounds__(kSortThreads, kBackJ == 8 ? 3 : 4) unsort_backward_kernel(SortArgs a) {
   using P = Pack<E, kVec>;
   using Raw = typename P::Raw;
   constexpr int kSeg = kVec == 1 ? 2 : 1;
   __shared__ float s_dot[kSortThreads / 32][kJBatch];
+  __shared__ Picks s;
   const int lanes = 1 << a.lanes_log2;
   const int lane = threadIdx.x & (lanes - 1), warp = threadIdx.x >> 5, slot = threadIdx.x >> a.lanes_log2;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads >> a.lanes_log2) + slot;
-  __shared__ Picks s;
   pdl_wait();
   pdl_trigger();
   load_picks(a, s, t, slot, lane, lanes);
@@ -200,45 +215,47 @@ __global__ void __launch_bounds__(kSortThreads) unsort_backward_kernel(SortArgs 
   E* dy = static_cast<E*>(a.out);
   const int64_t step = static_cast<int64_t>(lanes) * kVec;
   for (int j0 = 0; j0 < a.topk; j0 += kJBatch) {
-    int32_t d[kJBatch];
-    float w[kJBatch], dot[kJBatch];
+    float dot[kJBatch];
 #pragma unroll
-    for (int jj = 0; jj < kJBatch; ++jj) {
-      const bool on = live && j0 + jj < a.topk;
-      d[jj] = on ? s.d[slot][j0 + jj] : -1;
-      w[jj] = on ? s.w[slot][j0 + jj] : 0.0f;
-      dot[jj] = 0.0f;
-    }
+    for (int jj = 0; jj < kJBatch; ++jj) dot[jj] = 0.0f;
     for (int64_t c = static_cast<int64_t>(lane) * kVec; live && c < a.K; c += kSeg * step) {
-      Raw rd[kSeg], v[kSeg][kJBatch];
+      Raw rd[kSeg];
 #pragma unroll
       for (int i = 0; i < kSeg; ++i)
         if (c + i * step < a.K) rd[i] = *reinterpret_cast<const Raw*>(drow + c + i * step);
-      if (y) {
 #pragma unroll
-        for (int jj = 0; jj < kJBatch; ++jj)
+      for (int h = 0; h < kJBatch; h += kBackJ) {
+        Raw v[kSeg][kBackJ];
+        int32_t d[kBackJ];
 #pragma unroll
-          for (int i = 0; i < kSeg; ++i)
-            if (d[jj] >= 0 && c + i * step < a.K)
-              v[i][jj] = *reinterpret_cast<const Raw*>(y + d[jj] * a.y_ld + c + i * step);
-      }
+        for (int jj = 0; jj < kBackJ; ++jj) {
+          d[jj] = j0 + h + jj < a.topk ? s.d[slot][j0 + h + jj] : -1;
+          if (y && d[jj] >= 0) {
+            const E* row = y + d[jj] * a.y_ld + c;
 #pragma unroll
-      for (int i = 0; i < kSeg; ++i) {
-        if (c + i * step >= a.K) continue;
-        float g[kVec];
-        P::open(rd[i], g);
-#pragma unroll
-        for (int jj = 0; jj < kJBatch; ++jj) {
-          if (d[jj] < 0) continue;
-          float f[kVec];
-          if (y) {
-            P::open(v[i][jj], f);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) dot[jj] = fmaf(g[e], f[e], dot[jj]);
+            for (int i = 0; i < kSeg; ++i)
+              if (c + i * step < a.K) v[i][jj] = *reinterpret_cast<const Raw*>(row + i * step);
           }
+        }
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) f[e] = w[jj] * g[e];
-          *reinterpret_cast<Raw*>(dy + d[jj] * a.out_ld + c + i * step) = P::close(f);
+        for (int i = 0; i < kSeg; ++i) {
+          if (c + i * step >= a.K) continue;
+          float g[kVec];
+          P::open(rd[i], g);
+#pragma unroll
+          for (int jj = 0; jj < kBackJ; ++jj) {
+            if (d[jj] < 0) continue;
+            float f[kVec];
+            if (y) {
+              P::open(v[i][jj], f);
+#pragma unroll
+              for (int e = 0; e < kVec; ++e) dot[h + jj] = fmaf(g[e], f[e], dot[h + jj]);
+            }
+            const float w = s.w[slot][j0 + h + jj];
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) f[e] = w * g[e];
+            *reinterpret_cast<Raw*>(dy + d[jj] * a.out_ld + c + i * step) = P::close(f);
+          }
         }
       }
     }
@@ -251,14 +268,14 @@ __global__ void __launch_bounds__(kSortThreads) unsort_backward_kernel(SortArgs 
 #pragma unroll
       for (int jj = 0; jj < kJBatch; ++jj) s_dot[warp][jj] = dot[jj];
     }
-    __syncthreads();
+    group_sync(slot, lanes);
     // the group's first threads add its warps' sums in order
     if (live && lane < kJBatch && j0 + lane < a.topk) {
       float sum = 0.0f;
       for (int k = 0; k < lanes / 32; ++k) sum += s_dot[warp + k][lane];
       a.dw[t * a.topk + j0 + lane] = sum;
     }
-    __syncthreads();
+    group_sync(slot, lanes);
   }
 }
 
@@ -268,7 +285,8 @@ enum SortOp { kOpSort, kOpUnsort, kOpBackward };
 template <typename E, int kVec>
 SortKernel kernel_of(SortOp op, int topk) {
   if (op == kOpSort) return sort_tokens_kernel<E, kVec>;
-  if (op == kOpBackward) return unsort_backward_kernel<E, kVec>;
+  if (op == kOpBackward)
+    return kVec == 1 || topk <= 4 ? unsort_backward_kernel<E, kVec, 4> : unsort_backward_kernel<E, kVec, kVec == 1 ? 4 : 8>;
   if (topk == 1) return unsort_tokens_kernel<E, kVec, 1>;
   if (topk == 2) return unsort_tokens_kernel<E, kVec, 2>;
   return topk <= 4 ? unsort_tokens_kernel<E, kVec, 4> : unsort_tokens_kernel<E, kVec, 8>;
@@ -290,7 +308,9 @@ moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
   if (op == kOpUnsort) seg = (vec ? 8 : 16) / (a.topk == 1 ? 1 : a.topk == 2 ? 2 : a.topk <= 4 ? 4 : 8);
   if (op == kOpBackward) seg = vec ? 1 : 2;
   a.lanes_log2 = 5;
-  while (a.lanes_log2 < 8 && (seg << a.lanes_log2) < units) ++a.lanes_log2;
+  while (a.lanes_log2 < 8 && (seg << a.lanes_log2) < units &&
+         (op != kOpBackward || (a.T << (a.lanes_log2 - 5)) < kBackWarps))
+    ++a.lanes_log2;
   const int64_t per_cta = kSortThreads >> a.lanes_log2;
   const int64_t grid = (a.T + per_cta - 1) / per_cta;
   // few tokens: their columns are spread over CTAs too (not in the backward
