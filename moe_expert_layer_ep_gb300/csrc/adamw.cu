@@ -159,18 +159,25 @@ __device__ __forceinline__ float warp_max(float x) {
   return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
 }
 
+constexpr float kTiny = 1.17549435e-38f;   // 2^-126, the smallest normal number
+
 // A block's scale from its largest value: at least the smallest normal
 // number, so that its reciprocal is finite.
-__device__ __forceinline__ float block_scale(float top) { return top > 0.0f ? fmaxf(top, 1.17549435e-38f) : top; }
+__device__ __forceinline__ float block_scale(float top) { return top > 0.0f ? fmaxf(top, kTiny) : top; }
 
-// Square root and reciprocal within 2 ulp: the correctly rounded forms cost
-// several times the instructions.  Subnormal arguments count as 0: the callers
-// keep them away where that matters.
-__device__ __forceinline__ float sqrt_fast(float x) {
+// Square root of a normal number: the hardware's reciprocal root (2 ulp), and
+// one Newton step of the root on the residual x - s s, which the fused multiply-add
+// forms exactly.  Correctly rounded for every mantissa from 2^-100 up (compared
+// with the rounded function over all of them at both exponent parities; one ulp
+// off in places below), in half of that function's instructions.  The codes
+// depend on it: next to a rounding boundary an ulp more or less is another code.
+__device__ __forceinline__ float sqrt_newton(float x) {
   float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  const float s = x * y;
+  return fmaf(fmaf(-s, s, x), 0.5f * y, s);
 }
+// Reciprocal within 2 ulp, of a normal number.
 __device__ __forceinline__ float rcp_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -234,8 +241,6 @@ struct Block {
   __device__ __forceinline__ void step(const Arrays& t, const AdamHyper& h, float gs, int32_t b, int lane) const {
     float top_m = 0.0f, top_v = 0.0f;
     float fm[2][4], fv[2][4], root[2][4];   // root: sqrt(v), of at least the smallest normal number
-    const float dm = kCoded ? sm * (h.b1 / 16129.0f) : h.b1;   // (a code's step and the decay as one factor)
-    const float dv = kCoded ? sv * h.b2 : h.b2;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float fp[4], fg[4];
@@ -244,10 +249,11 @@ struct Block {
       if constexpr (kCoded) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float a = byte_value<128>(m[r].r ^ 0x80808080u, k);
-          const float q = byte_value<0>(v[r].r, k) * (1.0f / 255.0f);
-          fm[r][k] = a * fabsf(a);
-          fv[r][k] = (q * q) * (q * q);
+          const float a = byte_value<128>(m[r].r ^ 0x80808080u, k) * (1.0f / 127.0f);
+          float q = byte_value<0>(v[r].r, k) * (1.0f / 255.0f);
+          q = q * q;
+          fm[r][k] = a * fabsf(a) * sm;
+          fv[r][k] = q * q * sv;
         }
       } else {
         m[r].open(fm[r]);
@@ -255,10 +261,12 @@ struct Block {
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float x = fg[k] * gs;
-        fm[r][k] = fmaf(fm[r][k], dm, x * h.omb1);
-        fv[r][k] = fmaf(fv[r][k], dv, x * x * h.omb2);
-        root[r][k] = sqrt_fast(fmaxf(fv[r][k], 1.17549435e-38f));
+        // each product and sum rounded by itself (no contraction), as a
+        // step in elementary 32-bit operations does
+        const float x = __fmul_rn(fg[k], gs);
+        fm[r][k] = __fadd_rn(__fmul_rn(fm[r][k], h.b1), __fmul_rn(x, h.omb1));
+        fv[r][k] = __fadd_rn(__fmul_rn(fv[r][k], h.b2), __fmul_rn(__fmul_rn(x, x), h.omb2));
+        root[r][k] = sqrt_newton(fmaxf(fv[r][k], kTiny));
         const float denom = fmaf(root[r][k], h.inv_root, h.eps);
         fp[k] = fmaf(fm[r][k] * h.neg_step, rcp_fast(denom), fp[k] * h.decay);
         if (kCoded) {
@@ -277,15 +285,16 @@ struct Block {
     if (kCoded) {
       const float nm = block_scale(warp_max(top_m)), nv = block_scale(warp_max(top_v));
       const float im = nm > 0.0f ? __fdiv_rn(1.0f, nm) : 0.0f;
-      const float iv = 65025.0f * __fsqrt_rn(nv > 0.0f ? __fdiv_rn(1.0f, nv) : 0.0f);
+      const float iv = __fsqrt_rn(nv > 0.0f ? __fdiv_rn(1.0f, nv) : 0.0f);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float qm[4], qv[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          qm[k] = fmaf(copysignf(sqrt_fast(fabsf(fm[r][k]) * im), fm[r][k]), 127.0f, kMagic);
+          qm[k] = __fadd_rn(__fmul_rn(copysignf(sqrt_newton(fmaxf(fabsf(fm[r][k]) * im, kTiny)), fm[r][k]), 127.0f),
+                            kMagic);
           // 255 (v / s)^(1/4), at least 1
-          const float q = fmaxf(sqrt_fast(root[r][k] * iv), 1.0f) + kMagic;
+          const float q = __fadd_rn(fmaxf(__fmul_rn(sqrt_newton(fmaxf(root[r][k] * iv, kTiny)), 255.0f), 1.0f), kMagic);
           qv[k] = fv[r][k] > 0.0f ? q : 0.0f;
         }
         const int32_t i = b + 128 * r + 4 * lane;
