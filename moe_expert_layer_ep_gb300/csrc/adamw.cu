@@ -37,12 +37,12 @@ namespace {
 constexpr int kStateBlock = 256;
 constexpr int kMaxTensors = 384;
 // Threads of a CTA and elements of its chunk: one block per warp where there is
-// little to do, else 16.  With 8-bit states,
-// 302 M bf16 elements with a 32-bit copy took 1039 us in CTAs of 256 threads and
-// 32768 elements, 817 us in 128 and 32768, 784 us in 64 and 32768, 737 us in 64
-// and 8192; with 32-bit states 151 M bf16 elements took 494 us in CTAs of 256
-// threads and 32768 elements, 501 us in 64 and 8192.
-__host__ __device__ constexpr int adam_threads(bool coded) { return coded ? 64 : 256; }
+// little to do, else 16.  Narrow CTAs over short runs of memory suit the 8-bit
+// states, whose arithmetic and loads have to overlap across CTAs: 302 M bf16
+// elements with a 32-bit copy took 855 us in CTAs of 128 threads, 822 us in 64 and
+// 717 us in 32 (28 per SM; the copy bandwidth alone needs 715 us).  With 32-bit
+// states 151 M bf16 elements took 501 us in 64 threads and 487 us in 256.
+__host__ __device__ constexpr int adam_threads(bool coded) { return coded ? 32 : 256; }
 __host__ __device__ constexpr int32_t chunk_small(bool coded) { return adam_threads(coded) / 32 * kStateBlock; }
 __host__ __device__ constexpr int32_t chunk_large(bool coded) { return chunk_small(coded) * 16; }
 
@@ -311,7 +311,7 @@ struct Block {
 
 // P, G: float or uint16_t (bf16).
 template <typename P, typename G, bool kMaster, bool kCoded>
-__global__ void __launch_bounds__(adam_threads(kCoded), kCoded ? 12 : 3)
+__global__ void __launch_bounds__(adam_threads(kCoded), kCoded ? 28 : 3)
     adamw_kernel(const __grid_constant__ AdamTable t, const AdamHyper h) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t c = blockIdx.x;
