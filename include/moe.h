@@ -384,7 +384,8 @@ moe_status_t moe_unsort_tokens_backward(const void* dout, int64_t dout_ld, const
  *                                 dw [E, N, C]; zeros for an expert without rows
  * Rows outside all experts are neither read into a result nor written, whatever
  * they hold.  A row's results are the same bits whatever the other rows are;
- * all results are the same bits every time.  N, I, C and row strides must be
+ * all results are the same bits every time.  Outputs must not overlap inputs,
+ * nor one expert's rows another's.  N, I, C and row strides must be
  * multiples of 8, E <= 1024, rows < 2^31 (MOE_ERR_UNSUPPORTED otherwise);
  * matrices 16-byte aligned (MOE_ERR_MISALIGNED).  status: device int32, not
  * cleared here, set where 0 to MOE_ERR_INVALID_ARG when an expert's numbers do

@@ -19,10 +19,9 @@
 // of 32, so uneven experts cost the MMAs of at most 31 rows too many, not of
 // half a 128-row block each (which took a sixth to a quarter more at 512 and
 // 256 rows per expert).  A tile is worked on by a CTA pair: M = 256 over the
-// two, each CTA staging its own 128 weight rows and half of the tokens.  Per
-// 64-element block of the reduction that is 32 KB per SM instead of the 48 KB
-// of a 128 x 256 tile on one SM, whose writes and reads of shared memory (96 KB
-// at about 138 B per clock) took 700 cycles for 512 cycles of MMA.
+// two, each CTA staging its own 128 weight rows and half of the tokens: 32 KB
+// per SM and 64-element block of the reduction, where a 128 x 256 tile on one SM
+// needs 48 KB.
 //   kFwd    A = W rows (K-major)                  B = x rows (K-major)
 //   kDgrad  A = W columns (MN-major: the feature  B = dy rows (K-major)
 //           runs along W's memory rows)
@@ -40,9 +39,25 @@
 // lies there, NaN included, does not count.  (In the other products such rows
 // only make output rows that are not stored.)
 //
-// Both: one persistent CTA per SM: warp 0 TMA producer, warp 1 MMA issue, warps
-// 2-5 epilogue (one per 32 accumulator lanes, independent of one another), two
-// accumulators so that a tile's epilogue runs beside the next tile's MMAs.
+// Both: one persistent CTA per SM: warp 0 TMA producer, warp 1 MMA issue, the
+// others epilogue (one or two per 32 accumulator lanes, independent of one
+// another), two accumulators so that a tile's epilogue runs beside the next
+// tile's MMAs.
+//
+// What bounds it.  A full tile's reduction block takes 517 cycles of the MMA's
+// 512, and 32 KB in that time is 63 B per clock, about what an SM gets from L2:
+// the two limits coincide, and lower tiles are held by the second (192 tokens:
+// 437 cycles for 384).  With all SMs busy the board's power cap then sets the
+// clock (1.5 - 1.7 GHz): 16384 x 4096 x 4096 takes 279 us forward (1970 TFLOP/s;
+// the library's dense product of that size runs at 2010), 315 us for the rows'
+// gradient and 331 us for the weights', whose operands are read across their
+// memory rows.  Few rows per expert are bound by the weights' bytes (16 tokens on
+// 32 experts: 7.3 TB/s), 256 rows per expert nearly so (1536 x 2048 weights:
+// 6.1 - 6.6 TB/s), and the weights' gradient by its writes (195 us for 805 MB,
+// which alone take 203 us at the write-only rate).
+// Clusters of four, whose pairs would share their tokens' copies, fit 144 of the
+// 152 SMs.  Handing the tall tiles out first, looking up the next tile's numbers
+// ahead, or running through the features inside made no difference.
 #include <string.h>
 
 #include <initializer_list>

@@ -215,6 +215,66 @@ def test_rows_do_not_depend_on_the_others():
         assert torch.equal(a, b[some])
 
 
+def test_a_row_at_every_tile_height():
+    """The same row first among 1 to 300 others, so in MMAs of every width: the same bits."""
+    N, C = 144, 200
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn((300, C), generator=g).to(torch.bfloat16).cuda()
+    dy = torch.randn((300, N), generator=g).to(torch.bfloat16).cuda()
+    gu = torch.randn((300, 2 * C), generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn((1, N, C), generator=g) * 0.1).to(torch.bfloat16).cuda()
+    first = None
+    for n in (1, 32, 33, 64, 65, 97, 128, 129, 161, 193, 225, 255, 256, 257, 289, 300):
+        at = [torch.tensor([v], dtype=torch.int32, device="cuda") for v in (0, n)]
+        at.append(torch.zeros(4, dtype=torch.int32, device="cuda"))
+        got = [M.moe_expert_gemm(x[:n], w, *at), *M.moe_expert_gemm_swiglu(x[:n], w, *at),
+               M.moe_expert_gemm_dgrad(dy[:n], w, *at), M.moe_expert_gemm_dgrad_swiglu(dy[:n], w, gu[:n], *at)]
+        first = first or [t[0].clone() for t in got]
+        for a, b in zip(got, first):
+            assert torch.equal(a[0], b)
+
+
+def test_weights_gradient_of_every_number_of_rows():
+    """0 to 131 rows: every length of the last block of 64, next to rows that hold NaN."""
+    c = Case(list(range(132)), N=40, C=24, align=8, seed=12, gap=1)
+    dy, x = c.sorted(c.N, 1), c.sorted(c.C, 2)
+    dw = M.moe_expert_gemm_wgrad(dy.cuda(), x.cuda(), *c.at)
+    d64, x64 = np.nan_to_num(_f64(dy)), np.nan_to_num(_f64(x))
+    ref = R.expert_gemm_wgrad(d64, x64, c.start, c.counts)
+    size = R.expert_gemm_wgrad(np.abs(d64), np.abs(x64), c.start, c.counts)
+    near = (c.counts / 16 + 16)[:, None, None] * 2.0 ** -23 * size
+    assert np.all(np.abs(_f64(dw) - ref) <= near + BF * (np.abs(ref) + near))
+
+
+def test_full_size_sampled():
+    """A wide layer (16 experts of 7168 x 2048, 200 to 700 rows each): all outputs finite, sampled rows, and sampled
+    rows of a sampled expert's dW, against fp64."""
+    rng = np.random.default_rng(13)
+    counts = rng.integers(200, 700, 16)
+    counts[5] = 0
+    start = np.concatenate([[0], np.cumsum(-(-counts // 128) * 128)[:-1]])
+    rows, N, C = int(start[-1] + 768), 7168, 2048
+    at = [torch.from_numpy(v.astype(np.int32)).cuda() for v in (start, counts)]
+    at.append(torch.zeros(4, dtype=torch.int32, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(14)
+    x, dy = (torch.randn((rows, n), generator=g, device="cuda").to(torch.bfloat16) for n in (C, N))
+    w = (torch.randn((16, N, C), generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+    y, dx = M.moe_expert_gemm(x, w, *at), M.moe_expert_gemm_dgrad(dy, w, *at)
+    dw = M.moe_expert_gemm_wgrad(dy, x, *at)
+    assert int(at[2][0]) == 0 and torch.isfinite(dw).all() and not dw[5].any()
+    for e in (0, 4, 15):
+        a, b, we = int(start[e]), int(start[e] + counts[e]), w[e].double()
+        assert torch.isfinite(y[a:b]).all() and torch.isfinite(dx[a:b]).all()
+        for r in (a, (a + b) // 2, b - 1):
+            for got, v, m, K in ((y[r], x[r].double(), we.T, C), (dx[r], dy[r].double(), we, N)):
+                ref, near = v @ m, _acc(K) * (v.abs() @ m.abs())
+                assert torch.all((got.double() - ref).abs() <= near + BF * (ref.abs() + near))
+        for n in (0, 255, 256, 4099, N - 1):
+            d, xe = dy[a:b, n].double(), x[a:b].double()
+            ref, near = d @ xe, _acc(counts[e]) * (d.abs() @ xe.abs())
+            assert torch.all((dw[e, n].double() - ref).abs() <= near + BF * (ref.abs() + near))
+
+
 def test_strides_graph_and_stream():
     c = Case([70, 0, 129], N=136, C=72, seed=9)
     x, dy = torch.nan_to_num(c.sorted(c.C, 1)).cuda(), torch.nan_to_num(c.sorted(c.N, 2)).cuda()
