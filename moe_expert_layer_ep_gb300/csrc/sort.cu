@@ -57,6 +57,15 @@ struct Pack<uint16_t, 8> {
   }
 };
 template <>
+struct Pack<uint16_t, 2> {
+  using Raw = uint32_t;
+  __device__ static void open(const Raw& r, float (&f)[2]) {
+    const float2 a = unpack_bf16x2(r);
+    f[0] = a.x; f[1] = a.y;
+  }
+  __device__ static Raw close(const float (&f)[2]) { return pack_bf16x2(f[0], f[1]); }
+};
+template <>
 struct Pack<uint16_t, 1> {
   using Raw = uint16_t;
   __device__ static void open(const Raw& r, float (&f)[1]) { f[0] = __uint_as_float(static_cast<uint32_t>(r) << 16); }
@@ -137,7 +146,7 @@ template <typename E, int kVec, int kJ>
 __global__ void __launch_bounds__(kSortThreads) unsort_tokens_kernel(SortArgs a) {
   using P = Pack<E, kVec>;
   using Raw = typename P::Raw;
-  constexpr int kSeg = (kVec == 1 ? 16 : 8) / kJ;
+  constexpr int kSeg = (kVec <= 2 ? 16 : 8) / kJ;
   __shared__ Picks s;
   const int lanes = 1 << a.lanes_log2;
   const int lane = threadIdx.x & (lanes - 1), slot = threadIdx.x >> a.lanes_log2;
@@ -200,7 +209,7 @@ template <typename E, int kVec, int kBackJ>
 __global__ void __launch_bounds__(kSortThreads, kBackJ == 8 ? 3 : 4) unsort_backward_kernel(SortArgs a) {
   using P = Pack<E, kVec>;
   using Raw = typename P::Raw;
-  constexpr int kSeg = kVec == 1 ? 2 : 1;
+  constexpr int kSeg = kVec <= 2 ? 2 : 1;
   __shared__ float s_dot[kSortThreads / 32][kJBatch];
   __shared__ Picks s;
   const int lanes = 1 << a.lanes_log2;
@@ -286,23 +295,27 @@ template <typename E, int kVec>
 SortKernel kernel_of(SortOp op, int topk) {
   if (op == kOpSort) return sort_tokens_kernel<E, kVec>;
   if (op == kOpBackward)
-    return kVec == 1 || topk <= 4 ? unsort_backward_kernel<E, kVec, 4> : unsort_backward_kernel<E, kVec, kVec == 1 ? 4 : 8>;
+    return kVec <= 2 || topk <= 4 ? unsort_backward_kernel<E, kVec, 4> : unsort_backward_kernel<E, kVec, kVec <= 2 ? 4 : 8>;
   if (topk == 1) return unsort_tokens_kernel<E, kVec, 1>;
   if (topk == 2) return unsort_tokens_kernel<E, kVec, 2>;
   return topk <= 4 ? unsort_tokens_kernel<E, kVec, 4> : unsort_tokens_kernel<E, kVec, 8>;
 }
 
 // Row accesses are 16 bytes wide when every row starts on a 16-byte boundary
-// and its length is a multiple of 16 bytes, else one element wide.
+// and its length is a multiple of 16 bytes, else one element wide, or two bf16
+// elements where rows allow it.
 moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
   if (a.T == 0) return MOE_OK;
-  const int es = elem == MOE_ELEM_F32 ? 4 : 2, wide = 16 / es;
+  const int es = elem == MOE_ELEM_F32 ? 4 : 2;
   const bool has_y = a.y != nullptr;
   const uintptr_t bases = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) |
                           (has_y ? reinterpret_cast<uintptr_t>(a.y) : 0);
-  const bool vec = bases % 16 == 0 && a.K % wide == 0 && a.x_ld % wide == 0 && a.out_ld % wide == 0 &&
-                   (!has_y || a.y_ld % wide == 0);
-  const int64_t units = vec ? a.K / wide : a.K;
+  const auto fits = [&](int bytes) {
+    const int n = bytes / es;
+    return bases % bytes == 0 && a.K % n == 0 && a.x_ld % n == 0 && a.out_ld % n == 0 && (!has_y || a.y_ld % n == 0);
+  };
+  const bool vec = fits(16), two = !vec && es == 2 && fits(4);
+  const int64_t units = a.K / (vec ? 16 / es : two ? 2 : 1);
   // segments a thread has in flight, and the threads that cover a row with them
   int64_t seg = kSortBatch;
   if (op == kOpUnsort) seg = (vec ? 8 : 16) / (a.topk == 1 ? 1 : a.topk == 2 ? 2 : a.topk <= 4 ? 4 : 8);
@@ -323,7 +336,9 @@ moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
   if (elem == MOE_ELEM_F32)
     k = vec ? kernel_of<float, 4>(op, a.topk) : kernel_of<float, 1>(op, a.topk);
   else
-    k = vec ? kernel_of<uint16_t, 8>(op, a.topk) : kernel_of<uint16_t, 1>(op, a.topk);
+    k = vec   ? kernel_of<uint16_t, 8>(op, a.topk)
+        : two ? kernel_of<uint16_t, 2>(op, a.topk)
+              : kernel_of<uint16_t, 1>(op, a.topk);
   return launch_pdl(k, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(parts)), dim3(kSortThreads), 0, s, a) ==
                  cudaSuccess
              ? MOE_OK
