@@ -280,8 +280,6 @@ __device__ __noinline__ void leave_copies_time() {
   }
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // g and u of chunk c of a tile, arranged as pair_up leaves dh: word i of an even
 // (odd) lane holds two features of token 2i (2i + 1).  Zeros where there is none.
 __device__ __forceinline__ void load_gate_up(const ExpertArgs& g, const RowsTile& tl, int c, int64_t col, int64_t left,
@@ -501,18 +499,10 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       const int64_t left = g.n_cols - col;   // features there are from col
       const int chunks = tl.n / 32;
       constexpr int kStep = kEpiWarps / 4;
-      // kDgradSwiglu: g and u as pair_up leaves dh, a chunk ahead of it (the
-      // first while the MMAs run, and the others brought into L2 then)
+      // kDgradSwiglu: g and u as pair_up leaves dh, a chunk ahead of it, the
+      // first while the MMAs run (bringing the others into L2 then cost 2 %)
       uint32_t gw[kOp == kDgradSwiglu ? 16 : 1], uw[kOp == kDgradSwiglu ? 16 : 1];
-      if constexpr (kOp == kDgradSwiglu) {
-        load_gate_up(g, tl, half, col, left, lane, gw, uw);
-        for (int c = half + kStep; c < chunks; c += kStep)
-          if (c * 32 + lane < tl.valid && left > 0) {
-            const uint16_t* src = g.gu + (tl.row0 + c * 32 + lane) * g.gu_ld + col;
-            prefetch_l2(src);
-            prefetch_l2(src + g.n_cols);
-          }
-      }
+      if constexpr (kOp == kDgradSwiglu) load_gate_up(g, tl, half, col, left, lane, gw, uw);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns))) {
         set_status(g.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
