@@ -75,9 +75,7 @@ constexpr int kBlockK = 64;                          // elements: 128 bytes, one
 constexpr int kBoxBytes = 64 * kBlockK * 2;          // an MN-major box: 64 x 64 elements
 constexpr int kStgTile = 32 * 64;                    // a store tile: 32 rows x 32 columns
 constexpr uint32_t kTmemCols = 512;
-constexpr int kXchg = 5 * 1024;                      // kFwdSwiglu: a warp's two and a half tiles, and from there 16
-                                                     // tokens x 32 lanes in fp32
-constexpr int kMaxStages = 6, kMaxEpiWarps = 8;
+constexpr int kMaxStages = 6;
 
 // Shared memory: the stages, the epilogue warps' tiles, then the same for all.
 constexpr int kNumBars = 4 * kMaxStages + 9;         // full, empty (kWgrad: landed, cleared); tfull[2], tempty[2];
@@ -87,25 +85,27 @@ constexpr int kTailAbort = kTailHolder + 4;
 constexpr int kTailCum = kTailAbort + 4;             // token blocks of the 32-expert groups before, [33]
 constexpr int kTailBytes = kTailCum + 33 * 4 + 1024;   // + alignment slack
 
-// Stages, epilogue warps and their shared memory, by operator.  The activation
-// and its gradient take the epilogue more arithmetic and more bytes than the
-// product alone, and the weights' gradient has short sums for a whole output
-// tile: they get eight warps, two per 32 lanes.  Six stages where they fit (the
-// activation's gradient: 343 us with five, 330 us with six and a store tile less
-// per warp, at 16384 rows x 7168 x 2048).
+// Epilogue warps and their shared memory, by operator.  The activation and its
+// gradient take the epilogue more arithmetic and more bytes than the product
+// alone, and the weights' gradient has short sums for a whole output tile: they
+// get eight warps, two per 32 lanes.  All get six stages, for which the warps'
+// tiles are kept small: with five and larger tiles the activation took 193 us
+// instead of 185 (4096 tokens, top-8, 128 experts of 1536 x 2048), its gradient
+// 343 us instead of 330 (16384 rows, 32 experts of 7168 x 2048).
 template <ExpertOp kOp>
 struct Cfg {
-  static constexpr bool kAct = kOp == kFwdSwiglu || kOp == kDgradSwiglu;
-  static constexpr int kStages = kOp == kFwdSwiglu ? 5 : 6;
+  static constexpr int kStages = 6;
   static constexpr int kStage = 32 * 1024;
-  static constexpr int kEpiWarps = kAct || kOp == kWgrad ? 8 : 4;
+  static constexpr int kEpiWarps = kOp == kFwd || kOp == kDgrad ? 4 : 8;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kTiles = kOp == kDgradSwiglu ? 2 : 3;   // store tiles of an epilogue warp
-  static constexpr int kStgBytes = kOp == kFwdSwiglu ? kXchg + 2 * 1024 : kOp == kWgrad ? 4096 : kTiles * kStgTile;
+  static constexpr int kTiles = kOp == kFwd || kOp == kDgrad ? 3 : 2;   // store tiles of an epilogue warp (kWgrad: one
+                                                                        // of twice the size; kFwdSwiglu: one, and
+                                                                        // what its warps hand over)
+  static constexpr int kStgBytes = kTiles * kStgTile;
   static constexpr int kOffStg = kStages * kStage;
   static constexpr int kOffTail = kOffStg + kEpiWarps * kStgBytes;
   static constexpr int kSmem = kOffTail + kTailBytes;
-  static_assert(kSmem <= 227 * 1024 && kStages <= kMaxStages && kEpiWarps <= kMaxEpiWarps, "shared memory");
+  static_assert(kSmem <= 227 * 1024 && kStages <= kMaxStages, "shared memory");
 };
 
 // D fp32, A and B bf16; M and N are added
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     const int half = (warp - 2) >> 2;        // eight warps: each takes every other chunk
     uint8_t* stg = smem + F::kOffStg + (warp - 2) * F::kStgBytes;
     int iter = 0;
-    uint32_t slot = 0, met = 0;
+    uint32_t slot = 0;
     bool ok = true;
     // the warp's next store tile, once the store from it three tiles ago has read it
     auto next_tile = [&]() {
@@ -567,30 +567,25 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
         } else {
           // the g warp forms h of the chunk's first 16 tokens, the u warp of
           // the others: each gives the other its half.  Their barrier takes
-          // turns: values written (even phases), values read (odd).
+          // turns: values written (even phases), values read (odd).  What a
+          // warp gave away is where its part of h then goes.
           const bool is_up = quad >= 2;
           uint64_t* meet = &xchg[2 * half + (quad & 1)];
-          float* mine = reinterpret_cast<float*>(stg + kXchg);
+          float* mine = reinterpret_cast<float*>(stg + kStgTile);
           const float* theirs =
-              reinterpret_cast<const float*>(smem + F::kOffStg + ((warp - 2) ^ 2) * F::kStgBytes + kXchg);
-          if (met > 0)
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(meet, 1, abort_flag, g.timeout_ns));
-          if (!ok) break;
+              reinterpret_cast<const float*>(smem + F::kOffStg + ((warp - 2) ^ 2) * F::kStgBytes + kStgTile);
+          if (lane == 0) bulk_wait_read<0>();   // the chunk before's stores have read the tiles
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = __uint_as_float(is_up ? v[i] : v[16 + i]);
           mbar_arrive(meet);
-          // the last bulk groups are, latest first: h, g or u of the chunk
-          // before, and of the one before that, whose g or u tile is taken now
           if (g.out) {
-            if (lane == 0) bulk_wait_read<2>();
-            __syncwarp();
-            uint8_t* tile = stg + (met & 1) * kStgTile;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 p = pair_up(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), odd);
-              put_word(tile, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
+              put_word(stg, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
             }
-            store_tile<32>(tile, is_up ? &maps.out2 : &maps.out, rows, lane, static_cast<int>(col), 0,
+            store_tile<32>(stg, is_up ? &maps.out2 : &maps.out, rows, lane, static_cast<int>(col), 0,
                            static_cast<int>(row), g.out + row * g.out_ld + (is_up ? g.n_cols : 0) + col, g.out_ld, left);
           }
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(meet, 0, abort_flag, g.timeout_ns));
@@ -599,11 +594,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[i] = theirs[i * 32 + lane];
           mbar_arrive(meet);
-          ++met;
-          // h's tile is single: its last store has read it
-          if (lane == 0) g.out ? bulk_wait_read<1>() : bulk_wait_read<0>();
-          __syncwarp();
-          uint8_t* h_tile = stg + 2 * kStgTile;
+          uint32_t hw[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float hv[2];
@@ -614,8 +605,13 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
               hv[j] = gate * sigmoid_fast(gate) * up;
             }
             const float2 p = pair_up(hv[0], hv[1], odd);
-            put_word(h_tile, 2 * i + odd, lane >> 1, pack_bf16x2(p.x, p.y));
+            hw[i] = pack_bf16x2(p.x, p.y);
           }
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(meet, 1, abort_flag, g.timeout_ns));
+          if (!ok) break;
+          uint8_t* h_tile = stg + kStgTile;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) put_word(h_tile, 2 * i + odd, lane >> 1, hw[i]);
           const int h0 = is_up ? 16 : 0;
           store_tile<16>(h_tile, &maps.h, rows - h0, lane, static_cast<int>(col), 0, static_cast<int>(row) + h0,
                          g.h + (row + h0) * g.h_ld + col, g.h_ld, left);
