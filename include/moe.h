@@ -381,7 +381,12 @@ moe_status_t moe_unsort_tokens_backward(const void* dout, int64_t dout_ld, const
  *                                 dgu = dh u s (1 + g (1 - s)) | dh g s
  *                                 w2 [E, N, I], gu as the forward stored it
  *   moe_expert_gemm_wgrad         dw[e] = sum over e's rows of dy[r]^T x[r]
- *                                 dw [E, N, C]; zeros for an expert without rows
+ *                                 dw [E, N, C]; zeros for an expert without rows.
+ *                                 dw in bf16, or in fp32 without a rounding, there
+ *                                 with accumulate != 0 added to what dw holds (the
+ *                                 sum over several batches; one rounding to fp32,
+ *                                 subnormal sums may become 0; bf16:
+ *                                 MOE_ERR_UNSUPPORTED)
  * Rows outside all experts are neither read into a result nor written, whatever
  * they hold.  A row's results are the same bits whatever the other rows are;
  * all results are the same bits every time.  Outputs must not overlap inputs,
@@ -405,7 +410,7 @@ moe_status_t moe_expert_gemm_dgrad_swiglu(const void* dy, int64_t dy_ld, int64_t
                                           int64_t N, int64_t I, void* dgu, int64_t dgu_ld, void* status, void* stream);
 moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, int64_t rows,
                                    const int32_t* start, const int32_t* counts, int32_t E, int64_t N, int64_t C,
-                                   void* dw, void* status, void* stream);
+                                   void* dw, int32_t dw_elem, int32_t accumulate, void* status, void* stream);
 
 /* One AdamW step over many tensors.  Per element, in fp32:
  *   g' = grad_scale * g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2

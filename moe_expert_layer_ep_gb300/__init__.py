@@ -119,7 +119,7 @@ def _load():
         "moe_expert_gemm_swiglu": (I32, [VP, I64, I64, VP, VP, VP, I32, I64, I64, VP, I64, VP, I64, VP, VP]),
         "moe_expert_gemm_dgrad": (I32, [VP, I64, I64, VP, VP, VP, I32, I64, I64, VP, I64, VP, VP]),
         "moe_expert_gemm_dgrad_swiglu": (I32, [VP, I64, I64, VP, VP, I64, VP, VP, I32, I64, I64, VP, I64, VP, VP]),
-        "moe_expert_gemm_wgrad": (I32, [VP, I64, VP, I64, I64, VP, VP, I32, I64, I64, VP, VP, VP]),
+        "moe_expert_gemm_wgrad": (I32, [VP, I64, VP, I64, I64, VP, VP, I32, I64, I64, VP, I32, I32, VP, VP]),
         "moe_adamw_create": (I32, [P(MoeAdamwTensor), I32, P(VP)]),
         "moe_adamw_destroy": (None, [VP]),
         "moe_adamw_launches": (I32, [VP]),
@@ -481,9 +481,11 @@ def moe_sort_tokens(x, src2dst, rows=None, out=None, stream=None):
     if out is None:
         if rows is None:
             raise ValueError("rows or out must be given")
-        out = _empty((rows, K), x.dtype, x, stream)
-    _check(_lib.moe_sort_tokens(_ptr(x), x_ld, _ptr(src2dst), T, topk, K, _elem("x", x), _ptr(out),
-                                _rows("out", out, x.dtype, K), out.shape[0], _stream(stream)), "moe_sort_tokens")
+        out, out_ld = _empty((rows, K), x.dtype, x, stream), K
+    else:
+        out_ld = _rows("out", out, x.dtype, K)
+    _check(_lib.moe_sort_tokens(_ptr(x), x_ld, _ptr(src2dst), T, topk, K, _elem("x", x), _ptr(out), out_ld,
+                                out.shape[0], _stream(stream)), "moe_sort_tokens")
     return out
 
 
@@ -497,10 +499,11 @@ def moe_unsort_tokens(y, src2dst, topk_weights=None, out=None, stream=None):
     if topk_weights is not None:
         _require_cuda("topk_weights", topk_weights, torch.float32, T * topk)
     if out is None:
-        out = _empty((T, K), y.dtype, y, stream)
-    out_ld = _rows("out", out, y.dtype, K)
-    if out.shape[0] != T:
-        raise ValueError(f"out has {out.shape[0]} rows, src2dst {T}")
+        out, out_ld = _empty((T, K), y.dtype, y, stream), K
+    else:
+        out_ld = _rows("out", out, y.dtype, K)
+        if out.shape[0] != T:
+            raise ValueError(f"out has {out.shape[0]} rows, src2dst {T}")
     _check(_lib.moe_unsort_tokens(_ptr(y), y_ld, y.shape[0], _ptr(src2dst), _ptr(topk_weights), T, topk, K,
                                   _elem("y", y), _ptr(out), out_ld, _stream(stream)), "moe_unsort_tokens")
     return out
@@ -531,24 +534,28 @@ def moe_unsort_tokens_backward(dout, y, src2dst, topk_weights, dy=None, dw=None,
     return dy, dw
 
 
-def _expert_args(w, start, counts, status):
-    """Checks of the experts' products' common arguments: (E, N, C)."""
-    if w.dim() != 3:
-        raise ValueError("the weights must be [E, N, C]")
-    E, N, C = w.shape
-    _require_cuda("w", w, torch.bfloat16)
+def _expert_args(start, counts, status, E):
     _require_cuda("start", start, torch.int32, E)
     _require_cuda("counts", counts, torch.int32, E)
     if not status.is_cuda or status.numel() * status.element_size() < 4:
         raise ValueError("status must be a CUDA tensor of at least 4 bytes")
+
+
+def _expert_weights(w, start, counts, status):
+    """Checks of the arguments that the products with weights share: (E, N, C)."""
+    if w.dim() != 3:
+        raise ValueError("the weights must be [E, N, C]")
+    E, N, C = w.shape
+    _require_cuda("w", w, torch.bfloat16)
+    _expert_args(start, counts, status, E)
     return E, N, C
 
 
 def _sorted_out(name, t, rows, cols, like, stream):
     """An output of sorted rows, allocated when not given."""
     if t is None:
-        t = _empty((rows, cols), torch.bfloat16, like, stream)
-    elif t.shape[0] != rows:
+        return _empty((rows, cols), torch.bfloat16, like, stream), cols
+    if t.shape[0] != rows:
         raise ValueError(f"{name} has {t.shape[0]} rows, expected {rows}")
     return t, _rows(name, t, torch.bfloat16, cols)
 
@@ -556,7 +563,7 @@ def _sorted_out(name, t, rows, cols, like, stream):
 def moe_expert_gemm(x, w, start, counts, status, y=None, stream=None):
     """Sorted rows x [rows, C], w [E, N, C] -> y [rows, N] = x W_e^T for each expert's rows; see include/moe.h.
     status: CUDA tensor whose first int32 is the status word (a moe_sort_plan workspace, or 4 zeroed int32)."""
-    E, N, C = _expert_args(w, start, counts, status)
+    E, N, C = _expert_weights(w, start, counts, status)
     x_ld = _rows("x", x, torch.bfloat16, C)
     y, y_ld = _sorted_out("y", y, x.shape[0], N, x, stream)
     _check(_lib.moe_expert_gemm(_ptr(x), x_ld, x.shape[0], _ptr(w), _ptr(start), _ptr(counts), E, N, C, _ptr(y), y_ld,
@@ -567,7 +574,7 @@ def moe_expert_gemm(x, w, start, counts, status, y=None, stream=None):
 def moe_expert_gemm_swiglu(x, w13, start, counts, status, h=None, gu=None, keep_gu=True, stream=None):
     """Sorted rows x [rows, C], w13 [E, 2I, C] -> (h [rows, I], gu [rows, 2I]): the first product and its gated
     activation.  keep_gu=False: gu (which only the gradient needs) is not stored, and None is returned for it."""
-    E, N, C = _expert_args(w13, start, counts, status)
+    E, N, C = _expert_weights(w13, start, counts, status)
     if N % 2:
         raise ValueError("w13 must have 2I rows per expert")
     I = N // 2
@@ -584,7 +591,7 @@ def moe_expert_gemm_swiglu(x, w13, start, counts, status, h=None, gu=None, keep_
 
 def moe_expert_gemm_dgrad(dy, w, start, counts, status, dx=None, stream=None):
     """Gradient of moe_expert_gemm's rows: dy [rows, N], w [E, N, C] -> dx [rows, C]."""
-    E, N, C = _expert_args(w, start, counts, status)
+    E, N, C = _expert_weights(w, start, counts, status)
     dy_ld = _rows("dy", dy, torch.bfloat16, N)
     dx, dx_ld = _sorted_out("dx", dx, dy.shape[0], C, dy, stream)
     _check(_lib.moe_expert_gemm_dgrad(_ptr(dy), dy_ld, dy.shape[0], _ptr(w), _ptr(start), _ptr(counts), E, N, C,
@@ -595,7 +602,7 @@ def moe_expert_gemm_dgrad(dy, w, start, counts, status, dx=None, stream=None):
 def moe_expert_gemm_dgrad_swiglu(dy, w2, gu, start, counts, status, dgu=None, stream=None):
     """Gradient through the second product and the activation: dy [rows, N], w2 [E, N, I], gu [rows, 2I] as
     moe_expert_gemm_swiglu stored it -> dgu [rows, 2I]."""
-    E, N, I = _expert_args(w2, start, counts, status)
+    E, N, I = _expert_weights(w2, start, counts, status)
     dy_ld = _rows("dy", dy, torch.bfloat16, N)
     gu_ld = _rows("gu", gu, torch.bfloat16, 2 * I)
     if gu.shape[0] != dy.shape[0]:
@@ -607,19 +614,24 @@ def moe_expert_gemm_dgrad_swiglu(dy, w2, gu, start, counts, status, dgu=None, st
     return dgu
 
 
-def moe_expert_gemm_wgrad(dy, x, start, counts, status, dw=None, stream=None):
-    """Gradient of the weights: dy [rows, N], x [rows, C] -> dw [E, N, C], zeros for experts without rows."""
+def moe_expert_gemm_wgrad(dy, x, start, counts, status, dw=None, accumulate=False, stream=None):
+    """Gradient of the weights: dy [rows, N], x [rows, C] -> dw [E, N, C], zeros for experts without rows.  dw is
+    bfloat16 (also when it is allocated here) or float32; accumulate adds the gradient to a float32 dw."""
     E, N, C = counts.numel(), dy.shape[1], x.shape[1]
     dy_ld, x_ld = _rows("dy", dy, torch.bfloat16), _rows("x", x, torch.bfloat16)
     if x.shape[0] != dy.shape[0]:
         raise ValueError(f"x has {x.shape[0]} rows, dy {dy.shape[0]}")
     if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dw to add to")
         dw = _empty((E, N, C), torch.bfloat16, dy, stream)
     if tuple(dw.shape) != (E, N, C):
         raise ValueError(f"dw is {tuple(dw.shape)}, expected {(E, N, C)}")
-    _expert_args(dw, start, counts, status)
+    _require_cuda("dw", dw)
+    _expert_args(start, counts, status, E)
     _check(_lib.moe_expert_gemm_wgrad(_ptr(dy), dy_ld, _ptr(x), x_ld, x.shape[0], _ptr(start), _ptr(counts), E, N, C,
-                                      _ptr(dw), _ptr(status), _stream(stream)), "moe_expert_gemm_wgrad")
+                                      _ptr(dw), _elem("dw", dw), accumulate, _ptr(status), _stream(stream)),
+           "moe_expert_gemm_wgrad")
     return dw
 
 

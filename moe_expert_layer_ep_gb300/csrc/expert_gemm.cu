@@ -125,7 +125,8 @@ struct ExpertArgs {
   int32_t k_blocks;         // reduction blocks (not kWgrad)
   int64_t n_rows;           // kWgrad: output rows of an expert (N)
   int64_t n_cols;           // output columns (kFwdSwiglu: I)
-  uint16_t* out;            // y, gu, dx, dgu or dW
+  int32_t accumulate;       // kWgrad in fp32: dW is added to
+  uint16_t* out;            // y, gu, dx or dgu
   int64_t out_ld;
   uint16_t* h;              // kFwdSwiglu
   int64_t h_ld;
@@ -679,6 +680,8 @@ struct WgradTile {
   }
 };
 
+// kF32: dW in fp32, stored or (g.accumulate) added to what is there.
+template <bool kF32>
 __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ CUtensorMap map_out, const ExpertArgs g) {
@@ -876,7 +879,9 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     // ------------------------------------------------------------------ epilogue (both CTAs)
     // 64 columns at a time (every other 64 of the tile): two tensor-memory
     // loads, one 32-row x 128-byte store tile (128-byte swizzle: 16-byte piece
-    // j of row r at r * 128 + ((j ^ (r & 7)) * 16)), one store of whole lines
+    // j of row r at r * 128 + ((j ^ (r & 7)) * 16)), one store of whole lines.
+    // fp32: two such tiles of 32 columns.  Sums are added by the copy, in L2:
+    // one addition per element, so the results do not depend on the order.
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* tile = smem + F::kOffStg + (warp - 2) * F::kStgBytes;
     int iter = 0;
@@ -903,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
       }
 #pragma unroll 1
       for (int c = 64 * half; c < n; c += 64 * (kEpiWarps / 4)) {
-        uint4 o[8];
+        uint4 o[kF32 ? 16 : 8];
         if (any) {
           // (the second 32 columns may lie past the MMA's: loaded all the same,
           // from columns of this accumulator, and clipped by the store)
@@ -916,26 +921,44 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
           }
+          if constexpr (kF32) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            o[j] = pack8(v + 8 * j);
-            o[4 + j] = pack8(u + 8 * j);
+            for (int j = 0; j < 8; ++j) {
+              o[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              o[8 + j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              o[j] = pack8(v + 8 * j);
+              o[4 + j] = pack8(u + 8 * j);
+            }
           }
         } else {
+          if (kF32 && g.accumulate) break;   // nothing to add
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < (kF32 ? 16 : 8); ++j) o[j] = make_uint4(0, 0, 0, 0);
         }
         if (r0 >= g.n_rows) continue;        // warp-uniform
-        if (lane == 0) bulk_wait_read<0>();  // the store before has read the tile
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(tile + lane * 128 + ((j ^ (lane & 7)) << 4)) = o[j];
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          // (rows past N and columns past C are clipped by the map)
-          tma_store_3d(&map_out, tile, static_cast<int>(col0) + c, static_cast<int>(r0), expert);
-          bulk_commit_group();
+        for (int h = 0; h < (kF32 ? 2 : 1); ++h) {
+          if (kF32 && c + 32 * h >= n) break;   // past the last column
+          if (lane == 0) bulk_wait_read<0>();   // the store before has read the tile
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(tile + lane * 128 + ((j ^ (lane & 7)) << 4)) = o[8 * h + j];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            // (rows past N and columns past C are clipped by the map)
+            const int col = static_cast<int>(col0) + c + 32 * h;
+            if (kF32 && g.accumulate)
+              tma_add_3d(&map_out, tile, col, static_cast<int>(r0), expert);
+            else
+              tma_store_3d(&map_out, tile, col, static_cast<int>(r0), expert);
+            bulk_commit_group();
+          }
         }
       }
     }
@@ -984,16 +1007,17 @@ cudaError_t launch_rows(const RowsMaps& maps, const ExpertArgs& g, int64_t max_t
   return launch_pdl_cluster(expert_rows_kernel<kOp>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, maps, g);
 }
 
+template <bool kF32>
 cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const ExpertArgs& g,
                          int64_t tiles, cudaStream_t s) {
   using F = Cfg<kWgrad>;
   static int pairs = 0;
   if (pairs < 1) {
-    const cudaError_t e = resident_pairs(expert_wgrad_kernel, F::kThreads, F::kSmem, &pairs);
+    const cudaError_t e = resident_pairs(expert_wgrad_kernel<kF32>, F::kThreads, F::kSmem, &pairs);
     if (e != cudaSuccess) return e;
   }
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-  return launch_pdl_cluster(expert_wgrad_kernel, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, a, b, out, g);
+  return launch_pdl_cluster(expert_wgrad_kernel<kF32>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, a, b, out, g);
 }
 
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1183,27 +1207,35 @@ moe_status_t moe_expert_gemm_dgrad_swiglu(const void* dy, int64_t dy_ld, int64_t
 
 moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, int64_t rows,
                                    const int32_t* start, const int32_t* counts, int32_t E, int64_t N, int64_t C,
-                                   void* dw, void* status, void* stream) {
+                                   void* dw, int32_t dw_elem, int32_t accumulate, void* status, void* stream) {
   moe_status_t st = check_expert(rows, E, N, C, start, counts, status, {{dy, dy_ld, N}, {x, x_ld, C}});
   if (st != MOE_OK) return st;
-  if (!dw) return MOE_ERR_INVALID_ARG;
+  if (!dw || (dw_elem != MOE_ELEM_BF16 && dw_elem != MOE_ELEM_F32)) return MOE_ERR_INVALID_ARG;
+  const bool f32 = dw_elem == MOE_ELEM_F32;
+  if (accumulate && !f32) return MOE_ERR_UNSUPPORTED;
   if (off16(dw)) return MOE_ERR_MISALIGNED;
-  if (rows == 0)   // no expert has rows
-    return as_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * N * C * 2, static_cast<cudaStream_t>(stream)));
+  const uint64_t size = f32 ? 4 : 2;
+  if (rows == 0) {   // no expert has rows
+    if (accumulate) return MOE_OK;
+    return as_status(cudaMemsetAsync(dw, 0, size * E * N * C, static_cast<cudaStream_t>(stream)));
+  }
   CUtensorMap a, b, o;
   if ((st = rows_map(&a, dy, rows, N, dy_ld, kBlockK)) != MOE_OK) return st;
   if ((st = rows_map(&b, x, rows, C, x_ld, kBlockK)) != MOE_OK) return st;
   const uint64_t d[3] = {static_cast<uint64_t>(C), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(C) * 2, static_cast<uint64_t>(N) * static_cast<uint64_t>(C) * 2};
-  const uint32_t box[3] = {64, 32, 1};
-  if ((st = encode_tiled_map(&o, dw, kBf16, 3, d, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) != MOE_OK) return st;
+  const uint64_t strides[2] = {C * size, static_cast<uint64_t>(N) * C * size};
+  const uint32_t box[3] = {static_cast<uint32_t>(128 / size), 32, 1};
+  st = encode_tiled_map(&o, dw, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kBf16, 3, d, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != MOE_OK) return st;
   ExpertArgs g = expert_args(rows, E, start, counts, status);
   g.n_tiles = ceil_div(C, kTileN);
   g.m_tiles = ceil_div(N, kTileM);
   g.n_rows = N;
   g.n_cols = C;
-  return as_status(launch_wgrad(a, b, o, g, static_cast<int64_t>(E) * g.m_tiles * g.n_tiles,
-                                static_cast<cudaStream_t>(stream)));
+  g.accumulate = accumulate != 0;
+  return as_status((f32 ? launch_wgrad<true> : launch_wgrad<false>)(
+      a, b, o, g, static_cast<int64_t>(E) * g.m_tiles * g.n_tiles, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

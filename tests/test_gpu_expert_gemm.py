@@ -156,6 +156,52 @@ def test_wgrad(name):
     assert int(c.at[2][0]) == 0
 
 
+@cases
+def test_wgrad_in_fp32_stored_and_added(name):
+    """The unrounded sums: within their bound, the bf16 output before its rounding; added to what dw holds with one
+    rounding to fp32, which is the sum that torch forms.  Nothing around dw is written."""
+    c = Case(**CASES[name], seed=15)
+    dy, x = c.sorted(c.N, 1), c.sorted(c.C, 2)
+    d64, x64 = np.nan_to_num(_f64(dy)), np.nan_to_num(_f64(x))
+    dy, x = dy.cuda(), x.cuda()
+    size = c.E * c.N * c.C
+    around = torch.full((size + 64,), 5.0, device="cuda")
+    dw = around[32:32 + size].view(c.E, c.N, c.C)
+    M.moe_expert_gemm_wgrad(dy, x, *c.at, dw=dw)
+    ref = R.expert_gemm_wgrad(d64, x64, c.start, c.counts)
+    near = (c.counts / 16 + 16)[:, None, None] * 2.0 ** -23 * R.expert_gemm_wgrad(np.abs(d64), np.abs(x64), c.start,
+                                                                                  c.counts)
+    assert np.all(np.abs(_f64(dw) - ref) <= near)
+    assert torch.equal(dw.to(torch.bfloat16), M.moe_expert_gemm_wgrad(dy, x, *c.at))
+    one = dw.clone()
+    base = torch.randn((c.E, c.N, c.C), generator=torch.Generator().manual_seed(16)).cuda()
+    dw.copy_(base)
+    for _ in range(3):
+        M.moe_expert_gemm_wgrad(dy, x, *c.at, dw=dw, accumulate=True)
+        base = base + one
+        assert torch.equal(dw, base)
+    assert torch.all(around[:32] == 5.0) and torch.all(around[32 + size:] == 5.0)
+    assert int(c.at[2][0]) == 0
+
+
+def test_wgrad_in_fp32_refusals_and_no_rows():
+    c = Case([4], N=64, C=64)
+    x = torch.zeros((128, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(M.MoeError) as e:
+        M.moe_expert_gemm_wgrad(x, x, *c.at, dw=torch.zeros((1, 64, 64), device="cuda").bfloat16(), accumulate=True)
+    assert M.STATUS_NAMES[e.value.code] == "MOE_ERR_UNSUPPORTED"
+    with pytest.raises(M.MoeError) as e:
+        M.moe_expert_gemm_wgrad(x, x, *c.at, dw=torch.zeros(64 * 64 + 1, device="cuda")[1:].view(1, 64, 64))
+    assert M.STATUS_NAMES[e.value.code] == "MOE_ERR_MISALIGNED"
+    for bad in (dict(accumulate=True), dict(dw=torch.zeros((1, 64, 64), dtype=torch.float64, device="cuda")),
+                dict(dw=torch.zeros((1, 64, 32), device="cuda")), dict(dw=torch.zeros((1, 64, 128), device="cuda")[..., ::2])):
+        with pytest.raises(ValueError):
+            M.moe_expert_gemm_wgrad(x, x, *c.at, **bad)
+    empty, dw = x[:0], torch.full((1, 64, 64), 7.0, device="cuda")
+    assert torch.all(M.moe_expert_gemm_wgrad(empty, empty, *c.at, dw=dw, accumulate=True) == 7.0)
+    assert not M.moe_expert_gemm_wgrad(empty, empty, *c.at, dw=dw).any()
+
+
 def test_gradients_are_those_of_the_forward_product():
     """sum(dy * y) is linear in x and in w, so it equals sum(dx * x) and sum(dw * w): the stored outputs' rounding is
     the difference, at most 2^-8 of the terms' sizes."""

@@ -55,3 +55,30 @@ def test_the_example_learns(bits):
     losses = X.train(steps=40, state_bits=bits)
     assert all(v == v for v in losses)
     assert sum(losses[-4:]) < 0.5 * sum(losses[:4])
+
+
+def test_gradients_over_several_batches_add_up():
+    T, K, I, E, topk = 200, 128, 96, 8, 2
+    w13 = synth.bf16_expert_weights(E, 2 * I, K, 1, "cuda") * 4
+    w2 = synth.bf16_expert_weights(E, K, I, 2, "cuda") * 4
+    layer = X.ExpertLayer(w13, w2, T, topk, torch.float32)
+    sums = None
+    for part in range(3):
+        x = synth.activations(T, K, 3 + part, "cuda")
+        ids, weights = (t.cuda() for t in synth.routing(T, E, topk, 14 + part))
+        layer.forward(x, ids, weights)
+        dout = synth.activations(T, K, 25 + part, "cuda")
+        kept = [layer.dw13.clone(), layer.dw2.clone()]
+        one = [t.clone() for t in layer.backward(dout, weights)[:2]]
+        sums = one if sums is None else [a + b for a, b in zip(sums, one)]
+        if part > 0:
+            layer.dw13.copy_(kept[0])
+            layer.dw2.copy_(kept[1])
+            layer.backward(dout, weights, accumulate=True)
+        assert torch.equal(layer.dw13, sums[0]) and torch.equal(layer.dw2, sums[1])
+
+
+def test_the_example_learns_from_several_batches_a_step():
+    losses = X.train(steps=20, batches_per_step=2)
+    assert all(v == v for v in losses)
+    assert sum(losses[-2:]) < 0.5 * sum(losses[:2])
