@@ -53,8 +53,9 @@
 // gradient and 331 us for the weights', whose operands are read across their
 // memory rows.  Few rows per expert are bound by the weights' bytes (16 tokens on
 // 32 experts: 7.3 TB/s), 256 rows per expert nearly so (1536 x 2048 weights:
-// 6.1 - 6.6 TB/s), and the weights' gradient by its writes (195 us for 805 MB,
-// which alone take 203 us at the write-only rate).
+// 6.1 - 6.6 TB/s), and the weights' gradient by what L2 moves, writes counting
+// twice (128 x 1536 x 2048, 256 rows each: 183 us; 133 us without the stores,
+// 164 us with the copies of dy left out).
 // Clusters of four, whose pairs would share their tokens' copies, fit 144 of the
 // 152 SMs.  Handing the tall tiles out first, looking up the next tile's numbers
 // ahead, or running through the features inside made no difference.
@@ -97,7 +98,7 @@ struct Cfg {
   static constexpr int kStages = 6;
   static constexpr int kStage = 32 * 1024;
   static constexpr int kEpiWarps = kOp == kFwd || kOp == kDgrad ? 4 : 8;
-  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps + (kOp == kWgrad ? 32 : 0);
   static constexpr int kTiles = kOp == kFwd || kOp == kDgrad ? 3 : 2;   // store tiles of an epilogue warp (kWgrad: one
                                                                         // of twice the size; kFwdSwiglu: one, and
                                                                         // what its warps hand over)
@@ -680,11 +681,16 @@ struct WgradTile {
   }
 };
 
+// Tensor maps of a gradient of the weights.  a: dy, b: x, in boxes of 64 columns
+// and 16, 32, 48 or 64 rows: an expert's last rows take the lowest that holds them.
+struct WgradMaps {
+  CUtensorMap a[4], b[4], out;
+};
+
 // kF32: dW in fp32, stored or (g.accumulate) added to what is there.
 template <bool kF32>
 __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
-    expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                        const __grid_constant__ CUtensorMap map_out, const ExpertArgs g) {
+    expert_wgrad_kernel(const __grid_constant__ WgradMaps maps, const ExpertArgs g) {
   using F = Cfg<kWgrad>;
   constexpr int kStages = F::kStages, kEpiWarps = F::kEpiWarps;
   constexpr int kHalf = F::kStage / 2;   // a stage: 64 rows x 128 columns of dy, then of x
@@ -717,9 +723,11 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    prefetch_tensormap(&map_a);
-    prefetch_tensormap(&map_b);
-    prefetch_tensormap(&map_out);
+    for (int i = 0; i < 4; ++i) {
+      prefetch_tensormap(&maps.a[i]);
+      prefetch_tensormap(&maps.b[i]);
+    }
+    prefetch_tensormap(&maps.out);
   }
   if (warp == 1) {
     tmem_alloc_pair(holder, kTmemCols);
@@ -744,27 +752,29 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
       const int a0 = tl.mt * kTileM + static_cast<int>(rank) * 128;
       const int b0 = tl.nt * kTileN + static_cast<int>(rank) * (tl.n / 2);
       const bool two = tl.n > 128;   // boxes of 64 columns for this CTA's half of x
-      const uint32_t bytes = (two ? 4 : 3) * kBoxBytes;
+      const uint32_t boxes = two ? 4 : 3;
       for (int kb = 0; kb < tl.kb; ++kb) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns));
         if (!ok) break;
         uint8_t* a = smem + stage * F::kStage;
         uint8_t* b = a + kHalf;
         uint32_t bar = mapa(smem_u32(&full[stage]), 0);
+        int lowest = 3;
         if (kb == tl.kb - 1 && tl.tail < kBlockK) {
-          // rows past the expert's are cleared by this CTA's warp 1 once its
+          // rows past the expert's are cleared by this CTA's last warp once its
           // copies have landed; the stage's own barrier only keeps step
           bar = smem_u32(&landed[stage]);
-          mbar_arrive_expect_tx_elect(&landed[stage], bytes);
+          lowest = (tl.tail - 1) / 16;
+          mbar_arrive_expect_tx_elect(&landed[stage], boxes * (lowest + 1) * (16 * 128));
           if (rank == 0) mbar_arrive_expect_tx_elect(&full[stage], 0);
         } else if (rank == 0) {
-          mbar_arrive_expect_tx_elect(&full[stage], 2 * bytes);
+          mbar_arrive_expect_tx_elect(&full[stage], 2 * boxes * kBoxBytes);
         }
         const int row = static_cast<int>(tl.row0) + kb * kBlockK;
-        tma_load_3d_pair(a, &map_a, bar, a0, row, 0);
-        tma_load_3d_pair(a + kBoxBytes, &map_a, bar, a0 + 64, row, 0);
-        tma_load_3d_pair(b, &map_b, bar, b0, row, 0);
-        if (two) tma_load_3d_pair(b + kBoxBytes, &map_b, bar, b0 + 64, row, 0);
+        tma_load_3d_pair(a, &maps.a[lowest], bar, a0, row, 0);
+        tma_load_3d_pair(a + kBoxBytes, &maps.a[lowest], bar, a0 + 64, row, 0);
+        tma_load_3d_pair(b, &maps.b[lowest], bar, b0, row, 0);
+        if (two) tma_load_3d_pair(b + kBoxBytes, &maps.b[lowest], bar, b0 + 64, row, 0);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -779,71 +789,87 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
       leave_copies_time();
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer (even CTA); both clear
-    // (values broadcast from lane 0 are known to be uniform: the MMAs' operands
-    // and the loops around them stay in uniform registers)
-    const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0);
-    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    const bool issues = __shfl_sync(0xFFFFFFFFu, rank, 0) == 0;
-    int stage = 0, iter = 0;
-    uint32_t phase = 0, tails = 0;   // tails: parity of each stage's clearings
-    bool ok = true;
-    // `steps` MMAs of 16 reduction rows on a stage (16 rows of 128 bytes down the boxes)
-    auto multiply = [&](uint32_t d, uint32_t idesc, bool fresh, int steps) {
-      tc_fence_after();
-      const uint32_t a = base + stage * F::kStage;
-      const uint64_t ad = smem_desc(a, kBoxBytes, 1024, kSwizzle128B);
-      const uint64_t bd = smem_desc(a + kHalf, kBoxBytes, 1024, kSwizzle128B);
-      if (steps == 4) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16_pair(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(fresh && k == 0));
-      } else {
-        for (int k = 0; k < steps; ++k)
-          mma_bf16_pair(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(fresh && k == 0));
-      }
-      tc_commit_pair(&empty[stage]);
-    };
-    auto advance = [&]() {
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
-    };
-    for (bool more = tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
-      const int blocks = __shfl_sync(0xFFFFFFFFu, tl.kb, 0), tail = __shfl_sync(0xFFFFFFFFu, tl.tail, 0);
-      if (blocks == 0) continue;
-      const uint32_t idesc = kIdesc | kAMnMajor | kBMnMajor | idesc_mn(kTileM, __shfl_sync(0xFFFFFFFFu, tl.n, 0));
-      const int acc = iter & 1;
-      const uint32_t d = tm + static_cast<uint32_t>(acc * kTileN);
-      if (issues) {
+    // ------------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0) {
+      // (values broadcast from lane 0 are known to be uniform: the MMAs' operands
+      // and the loops around them stay in uniform registers)
+      const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      int stage = 0, iter = 0;
+      uint32_t phase = 0, tails = 0;   // tails: parity of each stage's clearings
+      bool ok = true;
+      for (bool more = tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
+        const int blocks = __shfl_sync(0xFFFFFFFFu, tl.kb, 0), tail = __shfl_sync(0xFFFFFFFFu, tl.tail, 0);
+        if (blocks == 0) continue;
+        const uint32_t idesc = kIdesc | kAMnMajor | kBMnMajor | idesc_mn(kTileM, __shfl_sync(0xFFFFFFFFu, tl.n, 0));
+        const int acc = iter & 1;
+        const uint32_t d = tm + static_cast<uint32_t>(acc * kTileN);
         ok = __all_sync(0xFFFFFFFFu,
                         mbar_wait_cluster_bounded(&tempty[acc], ((iter >> 1) & 1) ^ 1, abort_flag, g.timeout_ns));
         if (!ok) break;
         tc_fence_after();
-      }
-      ++iter;
-      const int whole = tail < kBlockK ? blocks - 1 : blocks;
-      for (int kb = 0; kb < whole; ++kb) {
-        if (issues) {
+        ++iter;
+        for (int kb = 0; kb < blocks; ++kb) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns));
           if (!ok) break;
-          multiply(d, idesc, kb == 0, 4);
+          int steps = 4;   // MMAs of 16 reduction rows; whole steps past the expert's end are left out
+          if (kb == blocks - 1 && tail < kBlockK) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster_bounded(&cleared[stage], (tails >> stage) & 1u, abort_flag,
+                                                                   g.timeout_ns));
+            if (!ok) break;
+            tails ^= 1u << stage;
+            steps = (tail + 15) / 16;
+          }
+          tc_fence_after();
+          // (16 rows of 128 bytes down the boxes)
+          const uint32_t a = base + stage * F::kStage;
+          const uint64_t ad = smem_desc(a, kBoxBytes, 1024, kSwizzle128B);
+          const uint64_t bd = smem_desc(a + kHalf, kBoxBytes, 1024, kSwizzle128B);
+          if (steps == 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_pair(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(kb == 0 && k == 0));
+          } else {
+            for (int k = 0; k < steps; ++k)
+              mma_bf16_pair(d, ad + (2048 >> 4) * k, bd + (2048 >> 4) * k, idesc, !(kb == 0 && k == 0));
+          }
+          tc_commit_pair(&empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
-        advance();
-      }
-      if (!ok) break;
-      if (whole < blocks) {
-        // the expert's last rows: whole steps of 16 past its end are left out,
-        // the rest of the last step is cleared in all four boxes (a row is 128
-        // consecutive bytes of its box, and stays in its place under the swizzle)
-        const uint32_t parity = (tails >> stage) & 1u;
-        tails ^= 1u << stage;
-        const int steps = (tail + 15) / 16;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&landed[stage], parity, abort_flag, g.timeout_ns));
         if (!ok) break;
-        const int clear = (steps * 16 - tail) * 8;   // 16-byte pieces of a box
-        uint8_t* first = smem + stage * F::kStage + tail * 128;
+        tc_commit_pair(&tfull[acc]);
+      }
+      if (!ok && lane == 0) {
+        set_status(g.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // all issued tensor-core work finished before the tensor memory is released
+      tc_commit_pair(done);
+      const int never = 0;
+      mbar_wait_bounded(done, 0, &never, g.timeout_ns);
+    }
+  } else if (warp == kEpiWarps + 2) {
+    // ------------------------------------------------------------------ clearing (both CTAs)
+    // An expert's last rows: the rest of their last step of 16 is cleared in all
+    // four boxes (a row is 128 consecutive bytes of its box, and stays in its
+    // place under the swizzle).  A warp of its own does so while the MMAs before
+    // are issued: with the issuer clearing, uneven experts took 197 us instead of
+    // 193 (128 experts of 1536 x 2048, 256 rows each on average).
+    int stage = 0;
+    uint32_t tails = 0;
+    bool ok = true;
+    for (bool more = tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
+      if (tl.kb == 0) continue;
+      if (tl.tail < kBlockK) {
+        const int at = (stage + tl.kb - 1) % kStages;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&landed[at], (tails >> at) & 1u, abort_flag, g.timeout_ns));
+        if (!ok) break;
+        tails ^= 1u << at;
+        const int clear = ((tl.tail + 15) / 16 * 16 - tl.tail) * 8;   // 16-byte pieces of a box
+        uint8_t* first = smem + at * F::kStage + tl.tail * 128;
 #pragma unroll
         for (int box = 0; box < 4; ++box)
           for (int i = lane; i < clear; i += 32)
@@ -852,28 +878,14 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         // are ordered before that by this fence, in this CTA)
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&cleared[stage]), 0));
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&cleared[at]), 0));
         __syncwarp();
-        if (issues) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns)) &&
-               __all_sync(0xFFFFFFFFu,
-                          mbar_wait_cluster_bounded(&cleared[stage], parity, abort_flag, g.timeout_ns));
-          if (!ok) break;
-          multiply(d, idesc, whole == 0, steps);
-        }
-        advance();
       }
-      if (issues) tc_commit_pair(&tfull[acc]);
+      stage = (stage + tl.kb) % kStages;
     }
     if (!ok && lane == 0) {
       set_status(g.status, MOE_ERR_TIMEOUT);
       *abort_flag = 1;
-    }
-    if (rank == 0) {
-      // all issued tensor-core work finished before the tensor memory is released
-      tc_commit_pair(done);
-      const int never = 0;
-      mbar_wait_bounded(done, 0, &never, g.timeout_ns);
     }
   } else {
     // ------------------------------------------------------------------ epilogue (both CTAs)
@@ -954,9 +966,9 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
             // (rows past N and columns past C are clipped by the map)
             const int col = static_cast<int>(col0) + c + 32 * h;
             if (kF32 && g.accumulate)
-              tma_add_3d(&map_out, tile, col, static_cast<int>(r0), expert);
+              tma_add_3d(&maps.out, tile, col, static_cast<int>(r0), expert);
             else
-              tma_store_3d(&map_out, tile, col, static_cast<int>(r0), expert);
+              tma_store_3d(&maps.out, tile, col, static_cast<int>(r0), expert);
             bulk_commit_group();
           }
         }
@@ -1008,8 +1020,7 @@ cudaError_t launch_rows(const RowsMaps& maps, const ExpertArgs& g, int64_t max_t
 }
 
 template <bool kF32>
-cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const ExpertArgs& g,
-                         int64_t tiles, cudaStream_t s) {
+cudaError_t launch_wgrad(const WgradMaps& maps, const ExpertArgs& g, int64_t tiles, cudaStream_t s) {
   using F = Cfg<kWgrad>;
   static int pairs = 0;
   if (pairs < 1) {
@@ -1017,7 +1028,7 @@ cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUten
     if (e != cudaSuccess) return e;
   }
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-  return launch_pdl_cluster(expert_wgrad_kernel<kF32>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, a, b, out, g);
+  return launch_pdl_cluster(expert_wgrad_kernel<kF32>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, maps, g);
 }
 
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1219,13 +1230,15 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
     if (accumulate) return MOE_OK;
     return as_status(cudaMemsetAsync(dw, 0, size * E * N * C, static_cast<cudaStream_t>(stream)));
   }
-  CUtensorMap a, b, o;
-  if ((st = rows_map(&a, dy, rows, N, dy_ld, kBlockK)) != MOE_OK) return st;
-  if ((st = rows_map(&b, x, rows, C, x_ld, kBlockK)) != MOE_OK) return st;
+  WgradMaps m;
+  for (int i = 0; i < 4; ++i) {
+    if ((st = rows_map(&m.a[i], dy, rows, N, dy_ld, 16 * (i + 1))) != MOE_OK) return st;
+    if ((st = rows_map(&m.b[i], x, rows, C, x_ld, 16 * (i + 1))) != MOE_OK) return st;
+  }
   const uint64_t d[3] = {static_cast<uint64_t>(C), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
   const uint64_t strides[2] = {C * size, static_cast<uint64_t>(N) * C * size};
   const uint32_t box[3] = {static_cast<uint32_t>(128 / size), 32, 1};
-  st = encode_tiled_map(&o, dw, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kBf16, 3, d, strides, box,
+  st = encode_tiled_map(&m.out, dw, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : kBf16, 3, d, strides, box,
                         CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != MOE_OK) return st;
   ExpertArgs g = expert_args(rows, E, start, counts, status);
@@ -1235,7 +1248,7 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
   g.n_cols = C;
   g.accumulate = accumulate != 0;
   return as_status((f32 ? launch_wgrad<true> : launch_wgrad<false>)(
-      a, b, o, g, static_cast<int64_t>(E) * g.m_tiles * g.n_tiles, static_cast<cudaStream_t>(stream)));
+      m, g, static_cast<int64_t>(E) * g.m_tiles * g.n_tiles, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
