@@ -15,8 +15,8 @@
 // Rows (all but kWgrad).  The sorted rows are few and uneven, the weights' rows
 // many and even, so the weights are the M side of the MMA and the tokens its N
 // side: D = W X^T, a tile of 256 features x n tokens.  An expert's rows are cut
-// into as few blocks of at most 256 as will do, equally tall up to a multiple
-// of 32, so uneven experts cost the MMAs of at most 31 rows too many, not of
+// into as few blocks of at most 256 as will do (lower ones where those are too few
+// for the pairs), equally tall up to a multiple of 32, so uneven experts cost the MMAs of at most 31 rows too many, not of
 // half a 128-row block each (which took a sixth to a quarter more at 512 and
 // 256 rows per expert).  A tile is worked on by a CTA pair: M = 256 over the
 // two, each CTA staging its own 128 weight rows and half of the tokens: 32 KB
@@ -84,7 +84,8 @@ constexpr int kNumBars = 4 * kMaxStages + 9;         // full, empty (kWgrad: lan
 constexpr int kTailHolder = kNumBars * 8;
 constexpr int kTailAbort = kTailHolder + 4;
 constexpr int kTailCum = kTailAbort + 4;             // token blocks of the 32-expert groups before, [33]
-constexpr int kTailBytes = kTailCum + 33 * 4 + 1024;   // + alignment slack
+constexpr int kTailTry = kTailCum + 33 * 4;          // the groups' token blocks of each height, [4][32]; then the height
+constexpr int kTailBytes = kTailTry + 4 * 32 * 4 + 1024;   // + alignment slack
 
 // Epilogue warps and their shared memory, by operator.  The activation and its
 // gradient take the epilogue more arithmetic and more bytes than the product
@@ -227,19 +228,44 @@ struct RowsTile {
   int ft;         // feature tile
 };
 
-__device__ __forceinline__ int token_blocks(int rows) { return (rows + kTokens - 1) / kTokens; }
+// Blocks of at most 256 >> low tokens.
+__device__ __forceinline__ int token_blocks(int rows, int low) { return (rows + (kTokens >> low) - 1) >> (8 - low); }
+
+// How tall tiles may be, 256 >> 0..3 tokens: what makes the time of all rounds
+// over the pairs least, at a reduction block's cycles for tiles of those heights
+// (what the MMA or L2 needs).  Lower tiles cost more per token, and pay for work
+// of a round or two: 1000 rows on one expert of 2048 x 2048 take 13 us instead of
+// 16, 2 x 512 rows' gradient on 4096 x 2048 19 instead of 24.5; 8 x 128 rows, for
+// which they are no use, 0.3 us more for the choice.
+// A converged warp; blocks: [4][32] of the groups of experts.
+__device__ __forceinline__ int tile_height(const int32_t* blocks, int n_tiles, int lane) {
+  constexpr unsigned kAll = 0xFFFFFFFFu;
+  const unsigned pairs = gridDim.x >> 1;
+  const int64_t tall = static_cast<int64_t>(__reduce_add_sync(kAll, blocks[lane])) * n_tiles;
+  if (tall > 2 * pairs) return 0;
+  // (lane i: that of 256 >> i)
+  unsigned sum = static_cast<unsigned>(tall);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    const unsigned tiles = __reduce_add_sync(kAll, blocks[i * 32 + lane]) * n_tiles;
+    if (lane == i) sum = tiles;
+  }
+  const unsigned cycles = lane == 0 ? 517 : lane == 1 ? 384 : lane == 2 ? 320 : 288;
+  const unsigned time = (sum + pairs - 1) / pairs * cycles * 4 + lane;
+  return __reduce_min_sync(kAll, lane < 4 ? time : ~0u) & 3;
+}
 
 // Tile t, looked up by a whole, converged warp: the group of 32 experts that
 // holds it from the groups' sums, then the expert from the counts of the group,
 // one per lane.  The same in all lanes.
-__device__ __forceinline__ RowsTile rows_tile(const ExpertArgs& g, const int32_t* s_cum, int64_t t, int lane) {
+__device__ __forceinline__ RowsTile rows_tile(const ExpertArgs& g, const int32_t* s_cum, int low, int64_t t, int lane) {
   constexpr unsigned kAll = 0xFFFFFFFFu;
   const bool past = lane * 32 < g.E && static_cast<int64_t>(s_cum[lane + 1]) * g.n_tiles > t;
   const int group = __ffs(__ballot_sync(kAll, past)) - 1;
   const int e = group * 32 + lane;
   const int rows = e < g.E ? expert_rows(g, e) : 0;
   const int start = e < g.E ? g.start[e] : 0;
-  const int mine = token_blocks(rows);
+  const int mine = token_blocks(rows, low);
   int end = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -350,25 +376,38 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     tmem_alloc_pair(holder, kTmemCols);
     tmem_relinquish_pair();
   }
+  int32_t* s_try = reinterpret_cast<int32_t*>(smem + F::kOffTail + kTailTry);
+  if (threadIdx.x < 128) s_try[threadIdx.x] = 0;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  // token blocks of each group of 32 experts, one warp per group, and their sums
-  const int groups = (g.E + 31) / 32;
-  for (int k = warp; k < groups; k += F::kThreads / 32) {
+  // token blocks of each group of 32 experts, one warp per group, the tiles'
+  // height, and the sums
+  for (int k = warp; k < (g.E + 31) / 32; k += F::kThreads / 32) {
     const int e = k * 32 + lane;
-    const int blocks = __reduce_add_sync(0xFFFFFFFFu, e < g.E ? token_blocks(expert_rows(g, e)) : 0);
-    if (lane == 0) s_cum[k + 1] = blocks;
+    const int rows = e < g.E ? expert_rows(g, e) : 0;
+    int blocks = 0;   // (lane i: of height 256 >> i)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int all = __reduce_add_sync(0xFFFFFFFFu, token_blocks(rows, i));
+      if (lane == i) blocks = all;
+    }
+    if (lane < 4) s_try[lane * 32 + k] = blocks;
   }
   __syncthreads();
   if (warp == 0) {
-    int x = lane < groups ? s_cum[lane + 1] : 0;
+    const int best = tile_height(s_try, g.n_tiles, lane);
+    int x = s_try[best * 32 + lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
     s_cum[lane + 1] = x;
-    if (lane == 0) s_cum[0] = 0;
+    if (lane == 0) {
+      s_cum[0] = 0;
+      s_try[0] = best;
+    }
   }
   report_experts(g);
   tc_fence_before();
@@ -377,6 +416,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *holder;
   const int64_t n_tiles = static_cast<int64_t>(s_cum[32]) * g.n_tiles;
+  const int low = s_try[0];
   const int64_t t0 = blockIdx.x >> 1, t_step = gridDim.x >> 1;
 
   if (warp == 0) {
@@ -386,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t t = t0; t < n_tiles && ok; t += t_step) {
-      const RowsTile tl = rows_tile(g, s_cum, t, lane);
+      const RowsTile tl = rows_tile(g, s_cum, low, t, lane);
       const uint32_t bytes = kRowsA + kRowsB / 4 * (4 - tl.box);
       const CUtensorMap* map_x = &maps.x[tl.box];
       const int tok = static_cast<int>(tl.row0) + static_cast<int>(rank) * (tl.n / 2);
@@ -435,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int64_t t = t0; t < n_tiles && ok; t += t_step, ++iter) {
-        const RowsTile tl = rows_tile(g, s_cum, t, lane);
+        const RowsTile tl = rows_tile(g, s_cum, low, t, lane);
         const uint32_t idesc =
             kIdesc | (kAMn ? kAMnMajor : 0u) | idesc_mn(256, __shfl_sync(0xFFFFFFFFu, tl.n, 0));
         const int acc = iter & 1;
@@ -493,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       return tile;
     };
     for (int64_t t = t0; t < n_tiles; t += t_step, ++iter) {
-      const RowsTile tl = rows_tile(g, s_cum, t, lane);
+      const RowsTile tl = rows_tile(g, s_cum, low, t, lane);
       const int acc = iter & 1;
       // this warp's 32 features, from col (kFwdSwiglu: quads 0 and 1 hold g, 2 and 3 the same features' u)
       const int64_t col = static_cast<int64_t>(tl.ft) * kFeatures + static_cast<int>(rank) * (kFeatures / 2) +
@@ -1103,8 +1143,8 @@ ExpertArgs expert_args(int64_t rows, int32_t E, const int32_t* start, const int3
 
 int32_t ceil_div(int64_t a, int64_t b) { return static_cast<int32_t>((a + b - 1) / b); }
 
-// Token blocks of any split of `rows` rows among E experts, at most.
-int64_t max_blocks(int64_t rows, int32_t E) { return rows / kTokens + E; }
+// Token blocks, of the lowest height, of any split of `rows` rows among E experts, at most.
+int64_t max_blocks(int64_t rows, int32_t E) { return rows / (kTokens >> 3) + E; }
 
 moe_status_t as_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 

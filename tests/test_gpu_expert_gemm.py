@@ -280,6 +280,40 @@ def test_a_row_at_every_tile_height():
             assert torch.equal(a[0], b)
 
 
+def test_tall_tiles_and_low_ones_agree():
+    """160 experts of n rows make tiles enough to take them 256 rows at a time, one expert alone is cut lower: every
+    row the same bits, and nothing written past an expert's rows."""
+    E, N, C, step = 160, 144, 72, 304
+    g = torch.Generator(device="cuda").manual_seed(17)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    x, dy, gu, w, w2 = rand(E * step, C), rand(E * step, N), rand(E * step, 2 * C), rand(E, 2 * N, C), rand(E, N, C)
+    start = torch.arange(E, dtype=torch.int32, device="cuda") * step
+    for n in (1, 31, 64, 97, 130, 192, 225, 256, 257, 300):
+        at = [start, torch.full_like(start, n), torch.zeros(4, dtype=torch.int32, device="cuda")]
+
+        def out(rows, cols):
+            return torch.full((rows, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+
+        def products(a, d, p, wa, wb, where, rows):
+            return [M.moe_expert_gemm(a, wa, *where, y=out(rows, 2 * N)),
+                    *M.moe_expert_gemm_swiglu(a, wa, *where, h=out(rows, N), gu=out(rows, 2 * N)),
+                    M.moe_expert_gemm_dgrad(d, wb, *where, dx=out(rows, C)),
+                    M.moe_expert_gemm_dgrad_swiglu(d, wb, p, *where, dgu=out(rows, 2 * C))]
+
+        tall = products(x, dy, gu, w, w2, at, E * step)
+        assert int(at[2][0]) == 0
+        for e in (0, 77, 159):
+            rows = slice(e * step, (e + 1) * step)
+            one = [torch.zeros(1, dtype=torch.int32, device="cuda"), at[1][:1], at[2]]
+            low = products(x[rows], dy[rows], gu[rows], w[e:e + 1], w2[e:e + 1], one, step)
+            for a, b in zip(tall, low):
+                assert torch.equal(a[rows], b)
+                assert torch.all(b[n:] == 7.0) and torch.isfinite(b[:n]).all()
+
+
 def test_weights_gradient_of_every_number_of_rows():
     """0 to 131 rows: every length of the last block of 64, next to rows that hold NaN."""
     c = Case(list(range(132)), N=40, C=24, align=8, seed=12, gap=1)
