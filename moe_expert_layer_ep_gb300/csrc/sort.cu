@@ -199,12 +199,13 @@ __global__ void __launch_bounds__(kSortThreads) unsort_tokens_kernel(SortArgs a)
 
 // kBackJ selections' rows in flight per thread.  A token is one short chain of
 // loads, stores and a reduction, so it is other tokens on the SM that keep the
-// memory busy: a token gets no more warps than leave kBackWarps in all, and
-// rows that are read element by element, or few per token, take fewer registers
-// for more CTAs per SM.  T = 4096, K = 2048, top-8, bf16: 55 us with a CTA per
-// token, 47 us so; T = 8192, K = 1001, top-4, fp32: 121 us, 69 us.
-constexpr int64_t kBackWarps = 7000;
-
+// memory busy: a token's threads get two segments of its rows each, or four and
+// 128 threads at most where a token has few rows, and rows that are read element
+// by element, or few per token, take fewer registers for more CTAs per SM.
+// T = 4096, K = 2048, top-8, bf16: 55 us with a CTA per token, 45 us so; T = 8192,
+// K = 7168: 306 us with one warp per token, 290 us so, top-2 100 and 99 us.  The
+// threads, and with them the order of the dot products' sums, depend on K and the
+// rows per token alone, so that a token's results do not depend on the others.
 template <typename E, int kVec, int kBackJ>
 __global__ void __launch_bounds__(kSortThreads, kBackJ == 8 ? 3 : 4) unsort_backward_kernel(SortArgs a) {
   using P = Pack<E, kVec>;
@@ -322,10 +323,11 @@ moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
   int64_t seg = kSortBatch;
   if (op == kOpUnsort) seg = (vec ? 8 : 16) / (a.topk == 1 ? 1 : a.topk == 2 ? 2 : a.topk <= 4 ? 4 : 8);
   if (op == kOpBackward) seg = vec ? 1 : 2;
+  const bool few = a.topk <= 4;
   a.lanes_log2 = 5;
   while (a.lanes_log2 < 8 && (seg << a.lanes_log2) < units &&
-         (op != kOpBackward || (a.T << (a.lanes_log2 - 5)) < kBackWarps) &&
-         (op != kOpUnsort || a.lanes_log2 < 7 || (a.T << (a.lanes_log2 - 5)) < 2 * kBackWarps))
+         (op != kOpBackward || ((seg << a.lanes_log2) * (few ? 4 : 2) < units && a.lanes_log2 < (few ? 7 : 8))) &&
+         (op != kOpUnsort || a.lanes_log2 < 7 || a.T < 3500))
     ++a.lanes_log2;
   const int64_t per_cta = kSortThreads >> a.lanes_log2;
   const int64_t grid = (a.T + per_cta - 1) / per_cta;

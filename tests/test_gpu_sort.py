@@ -230,6 +230,26 @@ def test_same_bits_alone_in_a_batch_in_a_graph_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("K,k,dtype", [(2048, 8, "bf16"), (2048, 2, "bf16"), (1001, 8, "bf16"), (1002, 3, "bf16"),
+                                       (1024, 5, "fp32"), (333, 4, "fp32")])
+def test_same_bits_alone_and_among_many(K, k, dtype):
+    T, E = 8000, 32
+    ids = _ids(T, E, k, 21, 0.1).cuda()
+    g = torch.Generator(device="cuda").manual_seed(22)
+    w = torch.rand((T, k), generator=g, device="cuda")
+    rows = M.moe_compact_all_tokens(T * k, E)
+    y, dout = (torch.randn((n, K), generator=g, device="cuda").to(DT[dtype]) for n in (rows, T))
+    s2d, _, _ = M.moe_sort_plan(ids, E)
+    out = M.moe_unsort_tokens(y, s2d, w)
+    dy, dw = M.moe_unsort_tokens_backward(dout, y, s2d, w, dy=torch.zeros_like(y))
+    for a, b in ((0, 1), (5000, 5002), (T - 300, T)):
+        some = [t[a:b].contiguous() for t in (dout, s2d, w)]
+        assert torch.equal(M.moe_unsort_tokens(y, some[1], some[2]), out[a:b])
+        dy1, dw1 = M.moe_unsort_tokens_backward(some[0], y, some[1], some[2], dy=torch.zeros_like(y))
+        at = some[1][some[1] >= 0].long()
+        assert torch.equal(dw1, dw[a:b]) and torch.equal(dy1[at], dy[at])
+
+
 def _code(f):
     with pytest.raises(M.MoeError) as e:
         f()
