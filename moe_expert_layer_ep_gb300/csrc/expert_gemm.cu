@@ -229,7 +229,9 @@ struct RowsTile {
 };
 
 // Blocks of at most 256 >> low tokens.
-__device__ __forceinline__ int token_blocks(int rows, int low) { return (rows + (kTokens >> low) - 1) >> (8 - low); }
+__device__ __forceinline__ int token_blocks(int rows, int low) {
+  return static_cast<int>((static_cast<unsigned>(rows) + (kTokens >> low) - 1) >> (8 - low));
+}
 
 // How tall tiles may be, 256 >> 0..3 tokens: what makes the time of all rounds
 // over the pairs least, at a reduction block's cycles for tiles of those heights
@@ -282,7 +284,7 @@ __device__ __forceinline__ RowsTile rows_tile(const ExpertArgs& g, const int32_t
   const int i = static_cast<int>(t - static_cast<int64_t>(first) * g.n_tiles);
   r.ft = i / blocks;
   const int b = i - r.ft * blocks;
-  const int tall = ((count + blocks - 1) / blocks + 31) & ~31;
+  const int tall = static_cast<int>(((static_cast<unsigned>(count) + blocks - 1) / blocks + 31) & ~31u);
   r.row0 = static_cast<int64_t>(__shfl_sync(kAll, start, at)) + b * tall;
   const int left = count - b * tall;
   r.valid = left < tall ? left : tall;
@@ -715,7 +717,7 @@ struct WgradTile {
     n = cols >= kTileN ? kTileN : (static_cast<int>(cols) + 31) & ~31;
     const int rows = expert_rows(g, expert);
     row0 = g.start[expert];
-    kb = (rows + kBlockK - 1) / kBlockK;
+    kb = static_cast<int>((static_cast<unsigned>(rows) + kBlockK - 1) / kBlockK);
     tail = rows - (kb - 1) * kBlockK;
     return true;
   }
