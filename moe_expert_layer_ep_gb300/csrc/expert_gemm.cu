@@ -48,10 +48,10 @@
 // 512, and 32 KB in that time is 63 B per clock, about what an SM gets from L2:
 // the two limits coincide, and lower tiles are held by the second (192 tokens:
 // 437 cycles for 384).  With all SMs busy the board's power cap then sets the
-// clock (1.5 - 1.7 GHz): 16384 x 4096 x 4096 takes 279 us forward (1970 TFLOP/s;
-// the library's dense product of that size runs at 2010), 315 us for the rows'
-// gradient and 331 us for the weights', whose operands are read across their
-// memory rows.  Few rows per expert are bound by the weights' bytes (16 tokens on
+// clock (1.3 - 1.7 GHz): 8 x 2048 rows of 4096 x 4096 take 286 us forward, 287 us
+// for the rows' gradient and 293 us for the weights' in the first milliseconds,
+// 330, 330 and 336 us (1667, 1666, 1638 TFLOP/s) when they run on at 1220 W; the
+// library's dense product of 16384 x 4096 x 4096 280 and 318 us.  Few rows per expert are bound by the weights' bytes (16 tokens on
 // 32 experts: 7.3 TB/s), 256 rows per expert nearly so (1536 x 2048 weights:
 // 6.1 - 6.6 TB/s), and the weights' gradient by what L2 moves, writes counting
 // twice (128 x 1536 x 2048, 256 rows each: 183 us; 133 us without the stores,
