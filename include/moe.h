@@ -427,9 +427,12 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
  * consecutive elements: m = s a |a| / 127^2, v = s (b / 255)^4.  Each step
  * sets a block's scales to its largest |m| and v (at least 2^-126 where not 0)
  * and rounds the roots to the nearest codes, b to at least 1 where v > 0.  All
- * codes and scales 0 is the state before the first step.  A gradient that is
+ * codes and scales 0 is the state before the first step.  A gradient g' that is
  * not finite makes its element of param, and its block's 8-bit states, not
- * finite.
+ * finite, and so does a state that is no number.  One whose square is beyond
+ * fp32 makes v infinite: such an element has no step but the decay, then and
+ * later, nor in 8 bits the other elements of its block from the next step on
+ * (code 0 is v = 0 whatever the scale).
  * moe_adamw_create keeps the tensors' pointers (which must stay valid) on the
  * host and groups them into launches of up to 384 tensors of one combination
  * of types; moe_adamw_launches says how many a step enqueues.  Pointers need

@@ -14,6 +14,10 @@
 // second moment rounded to nothing would leave m / eps as the step.  The
 // update itself uses the unrounded fp32 m and v of the step.
 //
+// A gradient whose square is beyond fp32 makes v infinite, and m / inf is no
+// step: the parameter only decays, then and later, and in 8 bits so do those of
+// its block, whose scale is infinite (code 0 stays v = 0).
+//
 // Bound by memory: every value is read once and written once.  A warp holds
 // one 256-element block in registers (two runs of 128 elements, four per
 // lane, so every access is a whole contiguous run), finds the block's largest
@@ -160,6 +164,7 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 constexpr float kTiny = 1.17549435e-38f;   // 2^-126, the smallest normal number
+constexpr float kMaxFloat = 3.40282347e+38f;
 
 // A block's scale from its largest value: at least the smallest normal
 // number, so that its reciprocal is finite.
@@ -171,11 +176,17 @@ __device__ __forceinline__ float block_scale(float top) { return top > 0.0f ? fm
 // with the rounded function over all of them at both exponent parities; one ulp
 // off in places below), in half of that function's instructions.  The codes
 // depend on it: next to a rounding boundary an ulp more or less is another code.
+// (NaN of infinity, whose reciprocal root is 0.)
 __device__ __forceinline__ float sqrt_newton(float x) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   const float s = x * y;
   return fmaf(fmaf(-s, s, x), 0.5f * y, s);
+}
+// The same, of infinity and NaN too.
+__device__ __forceinline__ float sqrt_any(float x) {
+  const float s = sqrt_newton(x);
+  return x <= kMaxFloat ? s : x;
 }
 // Reciprocal within 2 ulp, of a normal number.
 __device__ __forceinline__ float rcp_fast(float x) {
@@ -255,6 +266,11 @@ struct Block {
           fm[r][k] = a * fabsf(a) * sm;
           fv[r][k] = q * q * sv;
         }
+        if (sv > kMaxFloat) {   // (the whole warp; 0 inf is no number, and code 0 no second moment)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (((v[r].r >> (8 * k)) & 0xFFu) == 0) fv[r][k] = 0.0f;
+        }
       } else {
         m[r].open(fm[r]);
         v[r].open(fv[r]);
@@ -266,9 +282,10 @@ struct Block {
         const float x = __fmul_rn(fg[k], gs);
         fm[r][k] = __fadd_rn(__fmul_rn(fm[r][k], h.b1), __fmul_rn(x, h.omb1));
         fv[r][k] = __fadd_rn(__fmul_rn(fv[r][k], h.b2), __fmul_rn(__fmul_rn(x, x), h.omb2));
-        root[r][k] = sqrt_newton(fmaxf(fv[r][k], kTiny));
+        root[r][k] = sqrt_any(max_nan(fv[r][k], kTiny));
         const float denom = fmaf(root[r][k], h.inv_root, h.eps);
-        fp[k] = fmaf(fm[r][k] * h.neg_step, rcp_fast(denom), fp[k] * h.decay);
+        // (m by the quotient first: m times the step's length may be beyond fp32)
+        fp[k] = fmaf(fm[r][k] * rcp_fast(denom), h.neg_step, fp[k] * h.decay);
         if (kCoded) {
           top_m = max_nan(top_m, fabsf(fm[r][k]));
           top_v = max_nan(top_v, fv[r][k]);
