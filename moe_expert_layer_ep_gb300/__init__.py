@@ -162,6 +162,23 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, like, stream):
+    """An output or scratch tensor of a call that runs on stream (None: the current one).  Memory of the pool of the
+    stream that writes it: a free block of the current stream's pool may still be in use by work queued there, which
+    another stream does not wait for.  The current stream, where the tensor is then read, has passed its release
+    before that pool gives the memory away again."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
+        current = torch.cuda.current_stream(like.device)
+        if stream != current:
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=like.device)
+            t.record_stream(current)
+            return t
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _require_cuda(name, t, dtype=None, numel=None):
     if (t.is_cuda and (dtype is None or t.dtype is dtype) and (numel is None or t.numel() == numel)
             and t.is_contiguous()):
@@ -327,9 +344,9 @@ def moe_requant_weights_ue8m0(w_in, scale_in, w_out=None, scale_out=None, stream
     _require_cuda("w_in", w_in, torch.uint8)
     _require_cuda("scale_in", scale_in, torch.float32, E * (N // 128) * (C // 128))
     if w_out is None:
-        w_out = torch.empty_like(w_in)
+        w_out = _empty(tuple(w_in.shape), w_in.dtype, w_in, stream)
     if scale_out is None:
-        scale_out = torch.empty((E, N // 128, C // 128), dtype=torch.uint8, device=w_in.device)
+        scale_out = _empty((E, N // 128, C // 128), torch.uint8, w_in, stream)
     _require_cuda("w_out", w_out, torch.uint8, w_in.numel())
     _require_cuda("scale_out", scale_out, torch.uint8, E * (N // 128) * (C // 128))
     _check(_lib.moe_requant_weights_ue8m0(_ptr(w_in), _ptr(scale_in), _ptr(w_out), _ptr(scale_out), E, N, C,
@@ -343,7 +360,7 @@ def moe_router_prepare(w_router, out=None, stream=None):
     E, K = w_router.shape
     _require_cuda("w_router", w_router, torch.float32)
     if out is None:
-        out = torch.empty((3, E, K), dtype=torch.bfloat16, device=w_router.device)
+        out = _empty((3, E, K), torch.bfloat16, w_router, stream)
     _require_cuda("out", out, torch.bfloat16, 3 * E * K)
     _check(_lib.moe_router_prepare(_ptr(w_router), _ptr(out), E, K, _stream(stream)), "moe_router_prepare")
     return out
@@ -361,15 +378,14 @@ def moe_route(x, w_planes, topk, logits=None, topk_ids=None, topk_weights=None, 
     E = w_planes.shape[1]
     _require_cuda("x", x, torch.bfloat16)
     _require_cuda("w_planes", w_planes, torch.bfloat16, 3 * E * K)
-    dev = x.device
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        logits = _empty((T, E), torch.float32, x, stream)
     if topk_ids is None:
-        topk_ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        topk_ids = _empty((T, topk), torch.int32, x, stream)
     if topk_weights is None:
-        topk_weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+        topk_weights = _empty((T, topk), torch.float32, x, stream)
     if ws is None:
-        ws = torch.empty(max(16, moe_route_workspace_size(T, K, E)), dtype=torch.uint8, device=dev)
+        ws = _empty((max(16, moe_route_workspace_size(T, K, E)),), torch.uint8, x, stream)
     _require_cuda("logits", logits, torch.float32, T * E)
     _require_cuda("topk_ids", topk_ids, torch.int32, T * topk)
     _require_cuda("topk_weights", topk_weights, torch.float32, T * topk)
@@ -387,7 +403,7 @@ def moe_pack_mx_scales(sf, out=None, stream=None, C=None):
     C = ld * 32 if C is None else C
     _require_cuda("sf", sf, torch.uint8)
     if out is None:
-        out = torch.empty((E, N, C // 32), dtype=torch.uint8, device=sf.device)
+        out = _empty((E, N, C // 32), torch.uint8, sf, stream)
     _require_cuda("out", out, torch.uint8, E * N * (C // 32))
     _check(_lib.moe_pack_mx_scales(_ptr(sf), ld, _ptr(out), E, N, C, _stream(stream)), "moe_pack_mx_scales")
     return out
@@ -395,17 +411,6 @@ def moe_pack_mx_scales(sf, out=None, stream=None, C=None):
 
 # ------------------------------------------------------------------ training
 _ELEM = {torch.bfloat16: MOE_ELEM_BF16, torch.float32: MOE_ELEM_F32}
-
-
-def _empty(shape, dtype, like, stream):
-    """An output or scratch tensor of a call that runs on stream (None: the current one): memory of the current
-    stream's pool, kept from reuse there until a foreign stream has passed the call."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-        t.record_stream(stream)
-    return t
 
 
 def _rows(name, t, dtype=None, cols=None):
