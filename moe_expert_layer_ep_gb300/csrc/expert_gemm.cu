@@ -916,11 +916,13 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         for (int box = 0; box < 4; ++box)
           for (int i = lane; i < clear; i += 32)
             *reinterpret_cast<uint4*>(first + box * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
-        // (each SM's tensor core reads its own CTA's shared memory: the stores
-        // are ordered before that by this fence, in this CTA)
+        // Ordered before the MMAs' reads: the lanes' stores by the proxy fence and
+        // the warp's barrier, then by release at cluster scope, which the issuer
+        // (of the other CTA, for one half) acquires.  This warp has no stores to
+        // global memory that the release would wait for.
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&cleared[at]), 0));
+        if (lane == 0) mbar_arrive_remote_release(mapa(smem_u32(&cleared[at]), 0));
         __syncwarp();
       }
       stage = (stage + tl.kb) % kStages;
