@@ -157,6 +157,13 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
 }
 
+// The limit of a wait for whole tiles of the tensor core, g.timeout_ns longer than
+// the tiles may take: 4 us a reduction block, which takes 0.1 to 0.7, and 200 us
+// a tile for its output.  (An expert of 2^31 rows is a reduction of seconds.)
+__device__ __forceinline__ uint64_t tiles_limit(const ExpertArgs& g, int64_t blocks, int tiles) {
+  return g.timeout_ns + static_cast<uint64_t>(blocks) * 4000u + static_cast<uint64_t>(tiles) * 200000u;
+}
+
 // Eight accumulator values as bf16.
 __device__ __forceinline__ uint4 pack8(const uint32_t* v) {
   return make_uint4(pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
@@ -547,7 +554,8 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       // first while the MMAs run (bringing the others into L2 then cost 2 %)
       uint32_t gw[kOp == kDgradSwiglu ? 16 : 1], uw[kOp == kDgradSwiglu ? 16 : 1];
       if constexpr (kOp == kDgradSwiglu) load_gate_up(g, tl, half, col, left, lane, gw, uw);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns))) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag,
+                                                     tiles_limit(g, g.k_blocks, 1)))) {
         set_status(g.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
         break;
@@ -902,13 +910,19 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     // 193 (128 experts of 1536 x 2048, 256 rows each on average).
     int stage = 0;
     uint32_t tails = 0;
+    int64_t blocks = 0;   // since the last wait, and their tiles: those without a tail are passed by
+    int tiles = 0;
     bool ok = true;
     for (bool more = tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
       if (tl.kb == 0) continue;
+      blocks += tl.kb;
+      ++tiles;
       if (tl.tail < kBlockK) {
         const int at = (stage + tl.kb - 1) % kStages;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&landed[at], (tails >> at) & 1u, abort_flag, g.timeout_ns));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&landed[at], (tails >> at) & 1u, abort_flag,
+                                                       tiles_limit(g, blocks, tiles)));
         if (!ok) break;
+        blocks = tiles = 0;
         tails ^= 1u << at;
         const int clear = ((tl.tail + 15) / 16 * 16 - tl.tail) * 8;   // 16-byte pieces of a box
         uint8_t* first = smem + at * F::kStage + tl.tail * 128;
@@ -944,12 +958,14 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     bool more = tl.first(g, t0);
     while (more) {
       const int acc = iter & 1, n = tl.n, expert = tl.expert;
-      const bool any = tl.kb > 0;
+      const int kb = tl.kb;
+      const bool any = kb > 0;
       const int64_t r0 = static_cast<int64_t>(tl.mt) * kTileM + rank * 128 + quad * 32;
       const int64_t col0 = static_cast<int64_t>(tl.nt) * kTileN;
       more = tl.next(g, t_step);   // (its loads are on their way while this tile is waited for)
       if (any) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns))) {
+        if (!__all_sync(0xFFFFFFFFu,
+                        mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, tiles_limit(g, kb, 1)))) {
           set_status(g.status, MOE_ERR_TIMEOUT);
           *abort_flag = 1;
           break;

@@ -38,3 +38,52 @@ def test_cleared_last_rows_are_those_of_zeros(N, C):
     for _ in range(30):
         assert torch.equal(M.moe_expert_gemm_wgrad(*nans, *at), want)
     assert torch.isfinite(want).all() and int(at[2][0]) == 0
+
+
+def _sparse(rows, cols, at, seed):
+    """Zeros but for small whole numbers in the rows `at`: sums of their products are exact in any order."""
+    t = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t[at] = torch.randint(-8, 9, (len(at), cols), generator=g, device="cuda").to(torch.bfloat16)
+    return t
+
+
+def test_weights_gradient_over_as_many_rows_as_there_may_be():
+    """One expert of nearly 2^31 rows, a reduction of some 8 s: a wait for it has time enough."""
+    rows = 2 ** 31 - 71
+    at = torch.tensor([0, 77, 2 ** 29 + 5, rows - 58, rows - 57, rows - 1], device="cuda")
+    dy, x = _sparse(rows, 8, at, 1), _sparse(rows, 8, at, 2)
+    where = _at([0], [rows])
+    dw = M.moe_expert_gemm_wgrad(dy, x, *where, dw=torch.empty((1, 8, 8), device="cuda"))
+    assert M.moe_read_device_status(where[2]) == 0
+    assert torch.equal(dw[0].double(), dy[at].double().T @ x[at].double())
+
+
+def test_last_rows_after_a_long_reduction_without_any():
+    """A first expert of whole blocks of 64 for some 4 s, then others whose last rows are cleared, on the same pair of
+    CTAs among others."""
+    E, long = 200, 2 ** 30
+    rows = long + 64 * E
+    start = [0] + [long + 64 * e for e in range(E - 1)]
+    at = torch.tensor([3, long - 1] + [s + r for s in start[1:] for r in (0, 4)], device="cuda")
+    dy, x = _sparse(rows, 8, at, 3), _sparse(rows, 8, at, 4)
+    where = _at(start, [long] + [5] * (E - 1))
+    dw = M.moe_expert_gemm_wgrad(dy, x, *where, dw=torch.empty((E, 8, 8), device="cuda"))
+    assert M.moe_read_device_status(where[2]) == 0
+    d, a = dy[at].double().view(E, 2, 8), x[at].double().view(E, 2, 8)
+    assert torch.equal(dw.double(), d.transpose(1, 2) @ a)
+
+
+def test_products_over_as_many_columns_as_there_may_be():
+    """Reductions over nearly 2^30 columns, some 3 s each."""
+    n = 2 ** 30 - 8
+    at = torch.tensor([0, 1000, 2 ** 29 + 1, n - 65, n - 1], device="cuda")
+    x = _sparse(n, 1, at, 5).view(1, n)
+    where = _at([0], [1])
+    w = _sparse(n, 8, at, 6)
+    want = x[0, at].double() @ w[at].double()
+    got = M.moe_expert_gemm_dgrad(x, w.view(1, n, 8), *where)
+    assert M.moe_read_device_status(where[2]) == 0 and torch.equal(got[0], want.to(torch.bfloat16))
+    w = w.t().contiguous().view(1, 8, n)
+    got = M.moe_expert_gemm(x, w, *where)
+    assert M.moe_read_device_status(where[2]) == 0 and torch.equal(got[0], want.to(torch.bfloat16))
