@@ -1070,11 +1070,11 @@ cudaError_t resident_pairs(Kernel kernel, int threads, int smem, int* pairs) {
 template <ExpertOp kOp>
 cudaError_t launch_rows(const RowsMaps& maps, const ExpertArgs& g, int64_t max_tiles, cudaStream_t s) {
   using F = Cfg<kOp>;
-  static int pairs = 0;
-  if (pairs < 1) {
-    const cudaError_t e = resident_pairs(expert_rows_kernel<kOp>, F::kThreads, F::kSmem, &pairs);
-    if (e != cudaSuccess) return e;
-  }
+  static PerDevice known;
+  int pairs = 0;
+  const cudaError_t e = on_current_device(
+      known, &pairs, [](int* n) { return resident_pairs(expert_rows_kernel<kOp>, F::kThreads, F::kSmem, n); });
+  if (e != cudaSuccess) return e;
   const int grid = 2 * static_cast<int>(max_tiles < pairs ? max_tiles : pairs);
   return launch_pdl_cluster(expert_rows_kernel<kOp>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, maps, g);
 }
@@ -1082,11 +1082,11 @@ cudaError_t launch_rows(const RowsMaps& maps, const ExpertArgs& g, int64_t max_t
 template <bool kF32>
 cudaError_t launch_wgrad(const WgradMaps& maps, const ExpertArgs& g, int64_t tiles, cudaStream_t s) {
   using F = Cfg<kWgrad>;
-  static int pairs = 0;
-  if (pairs < 1) {
-    const cudaError_t e = resident_pairs(expert_wgrad_kernel<kF32>, F::kThreads, F::kSmem, &pairs);
-    if (e != cudaSuccess) return e;
-  }
+  static PerDevice known;
+  int pairs = 0;
+  const cudaError_t e = on_current_device(
+      known, &pairs, [](int* n) { return resident_pairs(expert_wgrad_kernel<kF32>, F::kThreads, F::kSmem, n); });
+  if (e != cudaSuccess) return e;
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
   return launch_pdl_cluster(expert_wgrad_kernel<kF32>, dim3(grid), dim3(F::kThreads), F::kSmem, s, 2, maps, g);
 }

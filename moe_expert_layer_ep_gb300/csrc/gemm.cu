@@ -818,13 +818,9 @@ __global__ void __launch_bounds__(threads_for(kFP8, kMX, kStage, kSplit), 1)
 template <bool kFP8, bool kMX, int kStage, bool kFP4, bool kSplit>
 cudaError_t launch_one(const GemmArgs& g, const GemmMaps& m, int grid, cudaStream_t s) {
   constexpr int kSmemBytes = Lay::kSmemBytes;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(grouped_gemm_kernel<kFP8, kMX, kStage, kFP4, kSplit>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static PerDevice smem_allowed;
+  const cudaError_t e = allow_smem(smem_allowed, grouped_gemm_kernel<kFP8, kMX, kStage, kFP4, kSplit>, kSmemBytes);
+  if (e != cudaSuccess) return e;
   if (g.pair)
     return launch_pdl_cluster(grouped_gemm_kernel<kFP8, kMX, kStage, kFP4, kSplit>, dim3(grid),
                               dim3(threads_for(kFP8, kMX, kStage, kSplit)), kSmemBytes, s, 2, m.a, m.b, m.out, m.wsf,
@@ -836,29 +832,33 @@ cudaError_t launch_one(const GemmArgs& g, const GemmMaps& m, int grid, cudaStrea
 // Co-resident two-CTA clusters of one (unsplit) kernel variant, x 2.
 template <bool kFP8, bool kMX, int kStage, bool kFP4>
 int pair_ctas_one() {
-  static int cached = -1;
-  if (cached >= 0) return cached;
-  auto kernel = grouped_gemm_kernel<kFP8, kMX, kStage, kFP4, false>;
-  constexpr int kSmemBytes = Lay::kSmemBytes;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return 0;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(threads_for(kFP8, kMX, kStage, false));
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
-    (void)cudaGetLastError();
-    clusters = 0;
-  }
-  cached = 2 * clusters;
-  return cached;
+  static PerDevice known;
+  int ctas = 0;
+  const cudaError_t e = on_current_device(known, &ctas, [](int* n) {
+    auto kernel = grouped_gemm_kernel<kFP8, kMX, kStage, kFP4, false>;
+    constexpr int kSmemBytes = Lay::kSmemBytes;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(threads_for(kFP8, kMX, kStage, false));
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      clusters = 0;
+    }
+    *n = 2 * clusters;
+    return cudaSuccess;
+  });
+  return e == cudaSuccess ? ctas : 0;
 }
 
 template <bool kFP8, bool kMX, bool kFP4>

@@ -8,8 +8,27 @@
 #include <utility>
 
 #include "../../include/moe.h"
+#include "per_device.h"
 
 namespace moe {
+
+// PerDevice::get for the device that is current.
+template <typename Make>
+cudaError_t on_current_device(PerDevice& numbers, int* value, Make make) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  return e != cudaSuccess ? e : numbers.get(device, value, make);
+}
+
+// More than 48 KB of dynamic shared memory for a kernel, once per device.
+template <typename Kernel>
+cudaError_t allow_smem(PerDevice& done, Kernel kernel, int bytes) {
+  int value;
+  return on_current_device(done, &value, [&](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
 
 // Launch a layer kernel with programmatic dependent launch allowed (it may
 // start while the stream's previous kernel runs; see pdl_wait in

@@ -457,14 +457,10 @@ cudaError_t launch_router_split(const float* w, uint16_t* planes, int64_t E, int
 cudaError_t launch_route(const CUtensorMap& map_x, const CUtensorMap& map_w, const RouterArgs& r, int grid, int topk,
                          float* logits, int32_t* ids, float* wts, cudaStream_t s) {
   if (r.T <= 0) return cudaSuccess;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(router_logits_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kRtSmemBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  cudaError_t e = cudaMemsetAsync(r.status, 0, 16, s);
+  static PerDevice smem_allowed;
+  cudaError_t e = allow_smem(smem_allowed, router_logits_tc_kernel, kRtSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(r.status, 0, 16, s);
   if (e != cudaSuccess) return e;
   e = launch_pdl(router_logits_tc_kernel, dim3(grid), dim3(kRtThreads), kRtSmemBytes, s, map_x, map_w, r);
   if (e != cudaSuccess) return e;
