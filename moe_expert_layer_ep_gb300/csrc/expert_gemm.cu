@@ -1045,6 +1045,13 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
   }
 }
 
+// The status of a call without sorted rows, which no product runs for.
+__global__ void report_kernel(const ExpertArgs g) {
+  pdl_wait();
+  pdl_trigger();
+  report_experts(g);
+}
+
 // CTA pairs of a kernel that fit on the device at once.
 template <typename Kernel>
 cudaError_t resident_pairs(Kernel kernel, int threads, int smem, int* pairs) {
@@ -1168,6 +1175,12 @@ int64_t max_blocks(int64_t rows, int32_t E) { return rows / (kTokens >> 3) + E; 
 
 moe_status_t as_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+// rows == 0: experts that claim some are reported as ever.
+moe_status_t no_rows(int32_t E, const int32_t* start, const int32_t* counts, void* status, void* stream) {
+  return as_status(launch_pdl(report_kernel, dim3(1), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                              expert_args(0, E, start, counts, status)));
+}
+
 }  // namespace
 
 }  // namespace moe
@@ -1183,7 +1196,7 @@ moe_status_t moe_expert_gemm(const void* x, int64_t x_ld, int64_t rows, const vo
   if (st != MOE_OK) return st;
   if (!w) return MOE_ERR_INVALID_ARG;
   if (off16(w)) return MOE_ERR_MISALIGNED;
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return no_rows(E, start, counts, status, stream);
   RowsMaps m;
   if ((st = token_maps(&m, x, rows, C, x_ld)) != MOE_OK) return st;
   if ((st = weights_map(&m.w, w, E, N, C, 128)) != MOE_OK) return st;
@@ -1207,7 +1220,7 @@ moe_status_t moe_expert_gemm_swiglu(const void* x, int64_t x_ld, int64_t rows, c
   if (off16(w13) || off16(gu)) return MOE_ERR_MISALIGNED;
   if (gu && gu_ld < 2 * I) return MOE_ERR_INVALID_ARG;
   if (gu && (gu_ld % 8 || gu_ld > (int64_t(1) << 36))) return MOE_ERR_UNSUPPORTED;
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return no_rows(E, start, counts, status, stream);
   RowsMaps m;
   if ((st = token_maps(&m, x, rows, C, x_ld)) != MOE_OK) return st;
   if ((st = weights_map(&m.w, w13, E, 2 * I, C, 64)) != MOE_OK) return st;
@@ -1234,7 +1247,7 @@ moe_status_t moe_expert_gemm_dgrad(const void* dy, int64_t dy_ld, int64_t rows, 
   if (st != MOE_OK) return st;
   if (!w) return MOE_ERR_INVALID_ARG;
   if (off16(w)) return MOE_ERR_MISALIGNED;
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return no_rows(E, start, counts, status, stream);
   RowsMaps m;
   if ((st = token_maps(&m, dy, rows, N, dy_ld)) != MOE_OK) return st;
   if ((st = weights_map(&m.w, w, E, N, C, kBlockK)) != MOE_OK) return st;
@@ -1257,7 +1270,7 @@ moe_status_t moe_expert_gemm_dgrad_swiglu(const void* dy, int64_t dy_ld, int64_t
   if (st != MOE_OK) return st;
   if (!w2) return MOE_ERR_INVALID_ARG;
   if (off16(w2)) return MOE_ERR_MISALIGNED;
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return no_rows(E, start, counts, status, stream);
   RowsMaps m;
   if ((st = token_maps(&m, dy, rows, N, dy_ld)) != MOE_OK) return st;
   if ((st = weights_map(&m.w, w2, E, N, I, kBlockK)) != MOE_OK) return st;
@@ -1287,8 +1300,11 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
   if (off16(dw)) return MOE_ERR_MISALIGNED;
   const uint64_t size = f32 ? 4 : 2;
   if (rows == 0) {   // no expert has rows
-    if (accumulate) return MOE_OK;
-    return as_status(cudaMemsetAsync(dw, 0, size * E * N * C, static_cast<cudaStream_t>(stream)));
+    if (!accumulate) {
+      const cudaError_t e = cudaMemsetAsync(dw, 0, size * E * N * C, static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return no_rows(E, start, counts, status, stream);
   }
   WgradMaps m;
   for (int i = 0; i < 4; ++i) {

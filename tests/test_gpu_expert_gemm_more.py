@@ -87,3 +87,20 @@ def test_products_over_as_many_columns_as_there_may_be():
     w = w.t().contiguous().view(1, 8, n)
     got = M.moe_expert_gemm(x, w, *where)
     assert M.moe_read_device_status(where[2]) == 0 and torch.equal(got[0], want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("counts,start,fits", [([0, 0], [0, 128], True), ([0, 3], [0, 0], False), ([-1, 0], [0, 0], False)])
+def test_no_sorted_rows_and_experts_that_claim_some(counts, start, fits):
+    """Experts whose numbers do not fit the buffers are reported where the buffers are empty, too."""
+    empty = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    w, gu = _randn(2, 64, 64), torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
+    sums = torch.full((2, 64, 64), 7.0, device="cuda")
+    for call in (lambda at: M.moe_expert_gemm(empty, w, *at), lambda at: M.moe_expert_gemm_swiglu(empty, w, *at),
+                 lambda at: M.moe_expert_gemm_dgrad(empty, w, *at),
+                 lambda at: M.moe_expert_gemm_dgrad_swiglu(empty, w, gu, *at),
+                 lambda at: M.moe_expert_gemm_wgrad(empty, empty, *at),
+                 lambda at: M.moe_expert_gemm_wgrad(empty, empty, *at, dw=sums, accumulate=True)):
+        at = _at(start, counts)
+        call(at)
+        assert M.moe_read_device_status(at[2]) == (0 if fits else M.STATUS["MOE_ERR_INVALID_ARG"])
+    assert torch.all(sums == 7.0)
