@@ -478,8 +478,8 @@ def moe_sort_tokens(x, src2dst, rows=None, out=None, stream=None):
     """x [T, K] bf16 or fp32 -> the rows in sorted order [rows, K]; rows that carry no token are left as they are.
     rows is needed when out is not given (moe_compact_all_tokens)."""
     T, topk = src2dst.shape
-    K = x.shape[1]
     x_ld = _rows("x", x)
+    K = x.shape[1]
     _require_cuda("src2dst", src2dst, torch.int32)
     if x.shape[0] != T:
         raise ValueError(f"x has {x.shape[0]} rows, src2dst {T}")
@@ -498,8 +498,8 @@ def moe_unsort_tokens(y, src2dst, topk_weights=None, out=None, stream=None):
     """Sorted rows y [rows, K] -> out [T, K], the (weighted) sum of each token's rows; without weights also the
     gradient of moe_sort_tokens."""
     T, topk = src2dst.shape
-    K = y.shape[1]
     y_ld = _rows("y", y)
+    K = y.shape[1]
     _require_cuda("src2dst", src2dst, torch.int32)
     if topk_weights is not None:
         _require_cuda("topk_weights", topk_weights, torch.float32, T * topk)
@@ -518,8 +518,8 @@ def moe_unsort_tokens_backward(dout, y, src2dst, topk_weights, dy=None, dw=None,
     """Gradient of moe_unsort_tokens with weights: (dy [rows, K], dw fp32 [T, k]).  dy's rows that carry no token are
     left as they are."""
     T, topk = src2dst.shape
-    K = dout.shape[1]
     dout_ld = _rows("dout", dout)
+    K = dout.shape[1]
     y_ld = _rows("y", y, dout.dtype, K)
     _require_cuda("src2dst", src2dst, torch.int32)
     _require_cuda("topk_weights", topk_weights, torch.float32, T * topk)
@@ -560,9 +560,10 @@ def _sorted_out(name, t, rows, cols, like, stream):
     """An output of sorted rows, allocated when not given."""
     if t is None:
         return _empty((rows, cols), torch.bfloat16, like, stream), cols
+    ld = _rows(name, t, torch.bfloat16, cols)
     if t.shape[0] != rows:
         raise ValueError(f"{name} has {t.shape[0]} rows, expected {rows}")
-    return t, _rows(name, t, torch.bfloat16, cols)
+    return t, ld
 
 
 def moe_expert_gemm(x, w, start, counts, status, y=None, stream=None):
@@ -622,8 +623,8 @@ def moe_expert_gemm_dgrad_swiglu(dy, w2, gu, start, counts, status, dgu=None, st
 def moe_expert_gemm_wgrad(dy, x, start, counts, status, dw=None, accumulate=False, stream=None):
     """Gradient of the weights: dy [rows, N], x [rows, C] -> dw [E, N, C], zeros for experts without rows.  dw is
     bfloat16 (also when it is allocated here) or float32; accumulate adds the gradient to a float32 dw."""
-    E, N, C = counts.numel(), dy.shape[1], x.shape[1]
     dy_ld, x_ld = _rows("dy", dy, torch.bfloat16), _rows("x", x, torch.bfloat16)
+    E, N, C = counts.numel(), dy.shape[1], x.shape[1]
     if x.shape[0] != dy.shape[0]:
         raise ValueError(f"x has {x.shape[0]} rows, dy {dy.shape[0]}")
     if dw is None:
