@@ -514,26 +514,40 @@ def moe_unsort_tokens(y, src2dst, topk_weights=None, out=None, stream=None):
     return out
 
 
-def moe_unsort_tokens_backward(dout, y, src2dst, topk_weights, dy=None, dw=None, stream=None):
+def moe_unsort_tokens_backward(dout, y, src2dst, topk_weights, dy=None, dw=None, stream=None, rows=None):
     """Gradient of moe_unsort_tokens with weights: (dy [rows, K], dw fp32 [T, k]).  dy's rows that carry no token are
-    left as they are."""
+    left as they are.  y=None: the rows' gradient alone, for weights that are not learned; dw is None then, and rows is
+    needed when dy is not given."""
     T, topk = src2dst.shape
     dout_ld = _rows("dout", dout)
     K = dout.shape[1]
-    y_ld = _rows("y", y, dout.dtype, K)
     _require_cuda("src2dst", src2dst, torch.int32)
     _require_cuda("topk_weights", topk_weights, torch.float32, T * topk)
     if dout.shape[0] != T:
         raise ValueError(f"dout has {dout.shape[0]} rows, src2dst {T}")
+    y_ld = 0
+    if y is None:
+        if dw is not None:
+            raise ValueError("the gradient of the weights needs y")
+        if dy is None and rows is None:
+            raise ValueError("rows or dy must be given")
+        if rows is None:
+            _rows("dy", dy, dout.dtype, K)
+            rows = dy.shape[0]
+    else:
+        y_ld = _rows("y", y, dout.dtype, K)
+        if rows not in (None, y.shape[0]):
+            raise ValueError(f"y has {y.shape[0]} rows, expected {rows}")
+        rows = y.shape[0]
+        if dw is None:
+            dw = _empty((T, topk), torch.float32, y, stream)
+        _require_cuda("dw", dw, torch.float32, T * topk)
     if dy is None:
-        dy = _empty(tuple(y.shape), y.dtype, y, stream)
-    if dw is None:
-        dw = _empty((T, topk), torch.float32, y, stream)
+        dy = _empty((rows, K), dout.dtype, dout, stream)
     dy_ld = _rows("dy", dy, dout.dtype, K)
-    _require_cuda("dw", dw, torch.float32, T * topk)
-    if dy.shape[0] != y.shape[0]:
-        raise ValueError(f"dy has {dy.shape[0]} rows, y {y.shape[0]}")
-    _check(_lib.moe_unsort_tokens_backward(_ptr(dout), dout_ld, _ptr(y), y_ld, y.shape[0], _ptr(src2dst),
+    if dy.shape[0] != rows:
+        raise ValueError(f"dy has {dy.shape[0]} rows, expected {rows}")
+    _check(_lib.moe_unsort_tokens_backward(_ptr(dout), dout_ld, _ptr(y), y_ld, rows, _ptr(src2dst),
                                            _ptr(topk_weights), T, topk, K, _elem("dout", dout), _ptr(dy), dy_ld,
                                            _ptr(dw), _stream(stream)), "moe_unsort_tokens_backward")
     return dy, dw
