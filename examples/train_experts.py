@@ -52,6 +52,8 @@ class ExpertLayer:
             return torch.empty((self.rows, cols), dtype=bf, device=dev)
 
         self.plan_ws = torch.empty(M.moe_sort_plan_workspace_size(T, topk, self.E), dtype=torch.uint8, device=dev)
+        self.plan_status = self.plan_ws[:4].view(torch.int32)   # of the last plan
+        self.status = torch.zeros(4, dtype=torch.int32, device=dev)   # of every call since
         self.src2dst = torch.empty((T, topk), dtype=torch.int32, device=dev)
         self.start = torch.empty(self.E, dtype=torch.int32, device=dev)
         self.counts = torch.empty(self.E, dtype=torch.int32, device=dev)
@@ -64,11 +66,11 @@ class ExpertLayer:
 
     @property
     def experts(self):
-        # (the plan's workspace begins with the status word that the products report to)
-        return self.start, self.counts, self.plan_ws
+        return self.start, self.counts, self.status
 
     def forward(self, x, ids, weights):
         M.moe_sort_plan(ids, self.E, src2dst=self.src2dst, start=self.start, counts=self.counts, ws=self.plan_ws)
+        torch.maximum(self.status[:1], self.plan_status, out=self.status[:1])   # (each plan clears its own)
         M.moe_sort_tokens(x, self.src2dst, out=self.xs)
         M.moe_expert_gemm_swiglu(self.xs, self.w13, *self.experts, h=self.h, gu=self.gu)
         M.moe_expert_gemm(self.h, self.w2, *self.experts, y=self.y)
@@ -126,9 +128,10 @@ def train(T=512, K=256, I=256, E=8, topk=2, steps=30, state_bits=8, lr=3e-3, cli
         scale = (clip / norm).clamp(max=1.0).reshape(1)   # stays on the device
         M.moe_adamw_step(opt, step=step, lr=lr, beta2=0.95, weight_decay=0.01, grad_scale=scale)
     losses = [float(v) for v in losses]
-    status = M.moe_read_device_status(layer.plan_ws)
-    if status:
-        raise RuntimeError(f"device status {M.STATUS_NAMES.get(status, status)}")
+    for part in (layer, teacher):
+        status = M.moe_read_device_status(part.status)
+        if status:
+            raise RuntimeError(f"device status {M.STATUS_NAMES.get(status, status)}")
     return losses
 
 
