@@ -104,3 +104,38 @@ def test_no_sorted_rows_and_experts_that_claim_some(counts, start, fits):
         call(at)
         assert M.moe_read_device_status(at[2]) == (0 if fits else M.STATUS["MOE_ERR_INVALID_ARG"])
     assert torch.all(sums == 7.0)
+
+
+def test_a_row_in_tiles_of_every_width():
+    """160 experts make tiles enough that one of n rows is one MMA of n rounded up to 32 tokens wide: a row's bits are
+    the same in all eight widths and in the low tiles of an expert alone, and nothing is written past an expert's
+    rows."""
+    E, N, C, step = 160, 144, 72, 256
+    x, dy, gu = _randn(E * step, C), _randn(E * step, N), _randn(E * step, 2 * C)
+    wide, w = _randn(E, 2 * N, C, seed=1), _randn(E, N, C, seed=2)
+    start = torch.arange(E) * step
+
+    def products(rows, experts, at):
+        a, d, p, wa, wb = x[rows], dy[rows], gu[rows], wide[experts], w[experts]
+
+        def out(cols):
+            return torch.full((a.shape[0], cols), 7.0, dtype=torch.bfloat16, device="cuda")
+
+        got = [M.moe_expert_gemm(a, wa, *at, y=out(2 * N)),
+               *M.moe_expert_gemm_swiglu(a, wa, *at, h=out(N), gu=out(2 * N)),
+               M.moe_expert_gemm_dgrad(d, wb, *at, dx=out(C)),
+               M.moe_expert_gemm_dgrad_swiglu(d, wb, p, *at, dgu=out(2 * C))]
+        assert int(at[2][0]) == 0
+        return got
+
+    every = slice(0, E * step)
+    full = products(every, slice(0, E), _at(start, [256] * E))
+    row = torch.arange(E * step, device="cuda") % step
+    for n in (1, 32, 33, 64, 65, 81, 96, 97, 128, 129, 160, 161, 192, 193, 200, 224, 225, 255):
+        tall = products(every, slice(0, E), _at(start, [n] * E))
+        for a, b in zip(tall, full):
+            assert torch.equal(a[row < n], b[row < n]) and torch.all(a[row >= n] == 7.0)
+        for e in (0, 93):
+            alone = products(slice(e * step, (e + 1) * step), slice(e, e + 1), _at([0], [n]))
+            for a, b in zip(alone, tall):
+                assert torch.equal(a, b[e * step:(e + 1) * step])
