@@ -172,9 +172,9 @@ __device__ __forceinline__ float block_scale(float top) { return top > 0.0f ? fm
 
 // Square root of a normal number: the hardware's reciprocal root (2 ulp), and
 // one Newton step of the root on the residual x - s s, which the fused multiply-add
-// forms exactly.  Correctly rounded for every mantissa from 2^-100 up (compared
-// with the rounded function over all of them at both exponent parities; one ulp
-// off in places below), in half of that function's instructions.  The codes
+// forms exactly.  Correctly rounded for every number from 2^-100 up, one ulp off
+// in places below (compared with the rounded function over all of them by
+// tests/test_gpu_adamw_math.py), in half of that function's instructions.  The codes
 // depend on it: next to a rounding boundary an ulp more or less is another code.
 // (NaN of infinity, whose reciprocal root is 0.)
 __device__ __forceinline__ float sqrt_newton(float x) {
