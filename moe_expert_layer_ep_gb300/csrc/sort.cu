@@ -318,8 +318,12 @@ moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
   const bool vec = fits(16), two = !vec && es == 2 && fits(4);
   const int64_t units = a.K / (vec ? 16 / es : two ? 2 : 1);
   // segments a thread has in flight, and the threads that cover a row with them
-  // (the way back: 128 threads where there are tokens enough: T = 8192, K = 7168,
-  // top-8 takes 168 us with 256 threads, 160 us with 128, 164 us with 64)
+  // (the way back: 128 threads at most.  In us with 128 and with 256, K = 7168,
+  // top-8: 4.6 and 5.8 for 128 tokens, 26.6 and 28.8 for 1001, 50.5 and 48.5 for
+  // 2000, 161 and 170 for 8192; K = 4096, top-4: 15.5 and 16.8 for 1500, 67 and
+  // 77 for 8192; K = 2048 in fp32, top-8: 25.6 and 26.2 for 2000, 49.6 and 47.7
+  // for 4000; K = 1001, top-8: 19.1 and 16.6 for 1500, 70.8 and 74.1 for 8192.
+  // Where 256 is ahead, its CTAs happen to fill the SMs more evenly.)
   int64_t seg = kSortBatch;
   if (op == kOpUnsort) seg = (vec ? 8 : 16) / (a.topk == 1 ? 1 : a.topk == 2 ? 2 : a.topk <= 4 ? 4 : 8);
   if (op == kOpBackward) seg = vec ? 1 : 2;
@@ -327,7 +331,7 @@ moe_status_t launch_sort(SortOp op, SortArgs a, int32_t elem, cudaStream_t s) {
   a.lanes_log2 = 5;
   while (a.lanes_log2 < 8 && (seg << a.lanes_log2) < units &&
          (op != kOpBackward || ((seg << a.lanes_log2) * (few ? 4 : 2) < units && a.lanes_log2 < (few ? 7 : 8))) &&
-         (op != kOpUnsort || a.lanes_log2 < 7 || a.T < 3500))
+         (op != kOpUnsort || a.lanes_log2 < 7))
     ++a.lanes_log2;
   const int64_t per_cta = kSortThreads >> a.lanes_log2;
   const int64_t grid = (a.T + per_cta - 1) / per_cta;
