@@ -40,15 +40,21 @@ namespace {
 
 constexpr int kStateBlock = 256;
 constexpr int kMaxTensors = 384;
-// Threads of a CTA and elements of its chunk: one block per warp where there is
-// little to do, else 16.  Narrow CTAs over short runs of memory suit the 8-bit
-// states, whose arithmetic and loads have to overlap across CTAs: 302 M bf16
-// elements with a 32-bit copy took 855 us in CTAs of 128 threads, 822 us in 64 and
-// 717 us in 32 (28 per SM; the copy bandwidth alone needs 715 us).  With 32-bit
-// states 151 M bf16 elements took 501 us in 64 threads and 487 us in 256.
+// Threads of a CTA.  Narrow CTAs over short runs of memory suit the 8-bit states,
+// whose arithmetic and loads have to overlap across CTAs: 302 M bf16 elements with
+// a 32-bit copy took 855 us in CTAs of 128 threads, 822 us in 64 and 717 us in 32
+// (28 per SM; the copy bandwidth alone needs 715 us).  With 32-bit states 151 M
+// bf16 elements took 501 us in 64 threads and 487 us in 256, of 16 blocks a warp.
 __host__ __device__ constexpr int adam_threads(bool coded) { return coded ? 32 : 256; }
+// Elements of its chunk: one block per warp, but 16 with 8-bit states (the next
+// block is then loaded ahead of this one's arithmetic) from 5 M elements on.  In us
+// for one and for 16, 8-bit states with a 32-bit copy: 1 M 5.2 and 13, 4.2 M 18.0
+// and 20.2, 5 M 21.3 and 21.6, 8.4 M 34.8 and 29.2, 151 M 598 and 368; without: 5 M
+// 21.3 and 20.3, 151 M 598 and 334.  32-bit states: 1 M 5.2 and 15.9, 16.8 M 55.7
+// and 67.8, 151 M 470 and 487; with the copy 602 and 623.
 __host__ __device__ constexpr int32_t chunk_small(bool coded) { return adam_threads(coded) / 32 * kStateBlock; }
-__host__ __device__ constexpr int32_t chunk_large(bool coded) { return chunk_small(coded) * 16; }
+constexpr int32_t chunk_large(bool coded) { return chunk_small(coded) * (coded ? 16 : 1); }
+constexpr int64_t kLarge = 5000000;
 
 struct AdamTable {
   void* p[kMaxTensors];
@@ -449,7 +455,7 @@ void add_launch(moe_adamw* a, int kind, const std::vector<const moe_adamw_tensor
   memset(&l.table, 0, sizeof(l.table));
   l.kind = kind;
   l.table.count = static_cast<int32_t>(ts.size());
-  l.table.chunk = total > (int64_t(1) << 23) ? moe::chunk_large(kind & 8) : moe::chunk_small(kind & 8);
+  l.table.chunk = total >= moe::kLarge ? moe::chunk_large(kind & 8) : moe::chunk_small(kind & 8);
   uint32_t end = 0;
   for (size_t i = 0; i < ts.size(); ++i) {
     const moe_adamw_tensor_t& t = *ts[i];
