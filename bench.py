@@ -412,11 +412,10 @@ def gemm_roofline(name, flops, nbytes, ms, peaks, fp8):
 
 
 def measure_write_peak(dev):
-    """Write-only HBM bandwidth of this GPU: torch's fill of a 512 MB buffer,
-    CUDA events over 10 fills after 3 untimed ones.  A stream of writes
-    alone runs well below the copy bandwidth (a read and a write per byte)
-    the roofline peaks are measured with."""
-    buf = torch.empty(512 << 20, dtype=torch.uint8, device=dev)
+    """Write-only HBM bandwidth of this GPU: torch's fill of a 512 MB buffer of
+    4-byte elements, CUDA events over 10 fills after 3 untimed ones.  (A fill
+    of 1- or 2-byte elements runs at half of it: its stores are narrower.)"""
+    buf = torch.empty(128 << 20, dtype=torch.float32, device=dev)
     for _ in range(3):
         buf.fill_(1)
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -425,7 +424,7 @@ def measure_write_peak(dev):
         buf.fill_(i)
     e1.record()
     torch.cuda.synchronize()
-    gbs = 10 * buf.numel() / (e0.elapsed_time(e1) / 1e3) / 1e9
+    gbs = 10 * buf.numel() * buf.element_size() / (e0.elapsed_time(e1) / 1e3) / 1e9
     del buf
     return gbs
 
@@ -687,7 +686,7 @@ def run_ours(args, w, world, rank, local):
                                 "what": "weights of non-empty experts + x + out (+ routing) at the measured "
                                         "HBM bandwidth, or the tensor time if larger"},
         "memory_passes": {"write_peak_gbs": round(write_gbs, 1),
-                          "write_peak_how": "torch fill of 512 MB, measured in this run",
+                          "write_peak_how": "torch fill of 512 MB of fp32, measured in this run",
                           "quant_scatter": memory_pass(float(med[1]), wm["quant_rw"], peaks, write_gbs),
                           "combine": memory_pass(float(med[4]), wm["combine_rw"], peaks, write_gbs)},
         "stage_ms": {n: round(float(v), 4) for n, v in zip(names, med)},
