@@ -63,8 +63,8 @@
 
 #include <initializer_list>
 
-#include "common.cuh"
 #include "internal.h"
+#include "pair.cuh"
 
 namespace moe {
 
