@@ -749,8 +749,8 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kOffTail);
   uint64_t* empty = full + kStages;
-  uint64_t* landed = empty + kStages;    // an expert's last rows: this CTA's copies
-  uint64_t* cleared = landed + kStages;  // ... and (the even CTA's) both CTAs' clearing
+  uint64_t* landed = empty + kStages;    // an expert's last rows (the even CTA's): both CTAs' copies
+  uint64_t* cleared = landed + kStages;  // ... and the clearing behind them
   uint64_t* tfull = cleared + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&landed[s], 1);
-      mbar_init(&cleared[s], 2);
+      mbar_init(&cleared[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -811,12 +811,14 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         uint32_t bar = mapa(smem_u32(&full[stage]), 0);
         int lowest = 3;
         if (kb == tl.kb - 1 && tl.tail < kBlockK) {
-          // rows past the expert's are cleared by this CTA's last warp once its
-          // copies have landed; the stage's own barrier only keeps step
-          bar = smem_u32(&landed[stage]);
+          // rows past the expert's are cleared by the even CTA's last warp once both
+          // CTAs' copies have landed; the stage's own barrier only keeps step
+          bar = mapa(smem_u32(&landed[stage]), 0);
           lowest = (tl.tail - 1) / 16;
-          mbar_arrive_expect_tx_elect(&landed[stage], boxes * (lowest + 1) * (16 * 128));
-          if (rank == 0) mbar_arrive_expect_tx_elect(&full[stage], 0);
+          if (rank == 0) {
+            mbar_arrive_expect_tx_elect(&landed[stage], 2 * boxes * (lowest + 1) * (16 * 128));
+            mbar_arrive_expect_tx_elect(&full[stage], 0);
+          }
         } else if (rank == 0) {
           mbar_arrive_expect_tx_elect(&full[stage], 2 * boxes * kBoxBytes);
         }
@@ -864,8 +866,8 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
           if (!ok) break;
           int steps = 4;   // MMAs of 16 reduction rows; whole steps past the expert's end are left out
           if (kb == blocks - 1 && tail < kBlockK) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster_bounded(&cleared[stage], (tails >> stage) & 1u, abort_flag,
-                                                                   g.timeout_ns));
+            ok = __all_sync(0xFFFFFFFFu,
+                            mbar_wait_bounded(&cleared[stage], (tails >> stage) & 1u, abort_flag, g.timeout_ns));
             if (!ok) break;
             tails ^= 1u << stage;
             steps = (tail + 15) / 16;
@@ -902,18 +904,22 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
       mbar_wait_bounded(done, 0, &never, g.timeout_ns);
     }
   } else if (warp == kEpiWarps + 2) {
-    // ------------------------------------------------------------------ clearing (both CTAs)
+    // ------------------------------------------------------------------ clearing (even CTA)
     // An expert's last rows: the rest of their last step of 16 is cleared in all
     // four boxes (a row is 128 consecutive bytes of its box, and stays in its
     // place under the swizzle).  A warp of its own does so while the MMAs before
     // are issued: with the issuer clearing, uneven experts took 197 us instead of
-    // 193 (128 experts of 1536 x 2048, 256 rows each on average).
+    // 193 (128 experts of 1536 x 2048, 256 rows each on average).  It clears both
+    // CTAs' boxes, so that all that orders it is in this CTA: an arrival from the
+    // other one would have to be a release at cluster scope, with which experts of
+    // up to 1360 rows took 231 us instead of 212 (217 with this CTA's boxes first:
+    // the other's take longer).
     int stage = 0;
     uint32_t tails = 0;
     int64_t blocks = 0;   // since the last wait, and their tiles: those without a tail are passed by
     int tiles = 0;
     bool ok = true;
-    for (bool more = tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
+    for (bool more = rank == 0 && tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
       if (tl.kb == 0) continue;
       blocks += tl.kb;
       ++tiles;
@@ -926,17 +932,18 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         tails ^= 1u << at;
         const int clear = ((tl.tail + 15) / 16 * 16 - tl.tail) * 8;   // 16-byte pieces of a box
         uint8_t* first = smem + at * F::kStage + tl.tail * 128;
+        const uint32_t other = mapa(smem_u32(first), 1);
+        for (int i = lane; i < clear; i += 32)
 #pragma unroll
-        for (int box = 0; box < 4; ++box)
-          for (int i = lane; i < clear; i += 32)
+          for (int box = 0; box < 4; ++box) clear_remote16(other + box * kBoxBytes + i * 16);
+        for (int i = lane; i < clear; i += 32)
+#pragma unroll
+          for (int box = 0; box < 4; ++box)
             *reinterpret_cast<uint4*>(first + box * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
-        // Ordered before the MMAs' reads: the lanes' stores by the proxy fence and
-        // the warp's barrier, then by release at cluster scope, which the issuer
-        // (of the other CTA, for one half) acquires.  This warp has no stores to
-        // global memory that the release would wait for.
-        fence_proxy_async_smem();
+        // ordered before the MMAs' reads of both CTAs' boxes
+        fence_proxy_async_cluster_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_release(mapa(smem_u32(&cleared[at]), 0));
+        if (lane == 0) mbar_arrive(&cleared[at]);
         __syncwarp();
       }
       stage = (stage + tl.kb) % kStages;

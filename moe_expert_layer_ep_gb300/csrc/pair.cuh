@@ -70,10 +70,14 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The same with what this thread wrote, and what it saw written, before: a thread
-// of another CTA that waits for it at cluster scope sees it too.
-__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Sixteen zero bytes to shared memory of a CTA of the cluster (addr: from mapa).
+__device__ __forceinline__ void clear_remote16(uint32_t cluster_addr) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr), "r"(0) : "memory");
+}
+// This thread's plain accesses to shared memory of the whole cluster are ordered
+// before what the async proxy (copies, MMAs) does there after.
+__device__ __forceinline__ void fence_proxy_async_cluster_smem() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 // mbar_wait_bounded for a barrier that other CTAs of the cluster arrive on.
 __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_t parity, const volatile int* abort,
