@@ -34,10 +34,10 @@
 //
 // Weights' gradient (kWgrad).  dW = dy^T x, a tile of 256 x at most 256 on a CTA
 // pair, both operands MN-major (64 x 64 boxes, no transposed copies), summed
-// over the expert's rows 64 at a time.  Rows beyond the expert's in the last
-// block are cleared in both CTAs' shared memory before the product, so whatever
-// lies there, NaN included, does not count.  (In the other products such rows
-// only make output rows that are not stored.)
+// over the expert's rows 64 at a time.  No other rows are copied, and the last 16
+// reduction rows are filled with zeros in both CTAs' shared memory, so whatever
+// lies behind the expert's rows, NaN included, does not count.  (In the other
+// products such rows only make output rows that are not stored.)
 //
 // Both: one persistent CTA per SM: warp 0 TMA producer, warp 1 MMA issue, the
 // others epilogue (one or two per 32 accumulator lanes, independent of one
@@ -79,7 +79,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 6;
 
 // Shared memory: the stages, the epilogue warps' tiles, then the same for all.
-constexpr int kNumBars = 4 * kMaxStages + 9;         // full, empty (kWgrad: landed, cleared); tfull[2], tempty[2];
+constexpr int kNumBars = 3 * kMaxStages + 9;         // full, empty (kWgrad: cleared); tfull[2], tempty[2];
                                                      // done; xchg[4]
 constexpr int kTailHolder = kNumBars * 8;
 constexpr int kTailAbort = kTailHolder + 4;
@@ -157,11 +157,11 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
 }
 
-// The limit of a wait for whole tiles of the tensor core, g.timeout_ns longer than
-// the tiles may take: 4 us a reduction block, which takes 0.1 to 0.7, and 200 us
-// a tile for its output.  (An expert of 2^31 rows is a reduction of seconds.)
-__device__ __forceinline__ uint64_t tiles_limit(const ExpertArgs& g, int64_t blocks, int tiles) {
-  return g.timeout_ns + static_cast<uint64_t>(blocks) * 4000u + static_cast<uint64_t>(tiles) * 200000u;
+// The limit of a wait for a whole tile of the tensor core: g.timeout_ns longer than
+// its reduction may take, at 4 us a block, which takes 0.1 to 0.7.  (An expert of
+// 2^31 rows is a reduction of seconds.)
+__device__ __forceinline__ uint64_t tile_limit(const ExpertArgs& g, int blocks) {
+  return g.timeout_ns + static_cast<uint64_t>(blocks) * 4000u;
 }
 
 // Eight accumulator values as bf16.
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
       uint32_t gw[kOp == kDgradSwiglu ? 16 : 1], uw[kOp == kDgradSwiglu ? 16 : 1];
       if constexpr (kOp == kDgradSwiglu) load_gate_up(g, tl, half, col, left, lane, gw, uw);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag,
-                                                     tiles_limit(g, g.k_blocks, 1)))) {
+                                                     tile_limit(g, g.k_blocks)))) {
         set_status(g.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
         break;
@@ -732,10 +732,18 @@ struct WgradTile {
 };
 
 // Tensor maps of a gradient of the weights.  a: dy, b: x, in boxes of 64 columns
-// and 16, 32, 48 or 64 rows: an expert's last rows take the lowest that holds them.
+// and wgrad_box_rows(i) rows, so that an expert's last rows are copied as they are,
+// in two pieces at most, and what is behind them can be cleared meanwhile.  In us,
+// 128 experts of 1536 x 2048 with 225 to 292 rows and with up to 1360, and for 16 of
+// 700: boxes of 16, 32, 48 and 64 rows, cleared once they have landed, 209, 212 and
+// 57; three pieces (1 - 8, 16, 32, 48 rows) 209, 214 and 55; so 201, 208 and 54; a
+// box of every height 196, 201 and 52, but forming 128 maps takes the host 5 us a
+// call more than four heights do, these 38 one.
+constexpr int kBoxes = 19;
 struct WgradMaps {
-  CUtensorMap a[4], b[4], out;
+  CUtensorMap a[kBoxes], b[kBoxes], out;
 };
+__host__ __device__ constexpr int wgrad_box_rows(int i) { return i < 16 ? i + 1 : 16 * (i - 14); }   // 1 .. 16, 32, 48, 64
 
 // kF32: dW in fp32, stored or (g.accumulate) added to what is there.
 template <bool kF32>
@@ -749,8 +757,7 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + F::kOffTail);
   uint64_t* empty = full + kStages;
-  uint64_t* landed = empty + kStages;    // an expert's last rows (the even CTA's): both CTAs' copies
-  uint64_t* cleared = landed + kStages;  // ... and the clearing behind them
+  uint64_t* cleared = empty + kStages;   // behind an expert's last rows, in both CTAs (the even CTA's)
   uint64_t* tfull = cleared + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
@@ -763,7 +770,6 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&landed[s], 1);
       mbar_init(&cleared[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -773,10 +779,8 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    for (int i = 0; i < 4; ++i) {
-      prefetch_tensormap(&maps.a[i]);
-      prefetch_tensormap(&maps.b[i]);
-    }
+    prefetch_tensormap(&maps.a[kBoxes - 1]);
+    prefetch_tensormap(&maps.b[kBoxes - 1]);
     prefetch_tensormap(&maps.out);
   }
   if (warp == 1) {
@@ -808,25 +812,20 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
         if (!ok) break;
         uint8_t* a = smem + stage * F::kStage;
         uint8_t* b = a + kHalf;
-        uint32_t bar = mapa(smem_u32(&full[stage]), 0);
-        int lowest = 3;
-        if (kb == tl.kb - 1 && tl.tail < kBlockK) {
-          // rows past the expert's are cleared by the even CTA's last warp once both
-          // CTAs' copies have landed; the stage's own barrier only keeps step
-          bar = mapa(smem_u32(&landed[stage]), 0);
-          lowest = (tl.tail - 1) / 16;
-          if (rank == 0) {
-            mbar_arrive_expect_tx_elect(&landed[stage], 2 * boxes * (lowest + 1) * (16 * 128));
-            mbar_arrive_expect_tx_elect(&full[stage], 0);
-          }
-        } else if (rank == 0) {
-          mbar_arrive_expect_tx_elect(&full[stage], 2 * boxes * kBoxBytes);
-        }
+        const uint32_t bar = mapa(smem_u32(&full[stage]), 0);
         const int row = static_cast<int>(tl.row0) + kb * kBlockK;
-        tma_load_3d_pair(a, &maps.a[lowest], bar, a0, row, 0);
-        tma_load_3d_pair(a + kBoxBytes, &maps.a[lowest], bar, a0 + 64, row, 0);
-        tma_load_3d_pair(b, &maps.b[lowest], bar, b0, row, 0);
-        if (two) tma_load_3d_pair(b + kBoxBytes, &maps.b[lowest], bar, b0 + 64, row, 0);
+        // a box's rows from row `at` of the block
+        const auto copy = [&](int box, int at) {
+          tma_load_3d_pair(a + at * 128, &maps.a[box], bar, a0, row + at, 0);
+          tma_load_3d_pair(a + at * 128 + kBoxBytes, &maps.a[box], bar, a0 + 64, row + at, 0);
+          tma_load_3d_pair(b + at * 128, &maps.b[box], bar, b0, row + at, 0);
+          if (two) tma_load_3d_pair(b + at * 128 + kBoxBytes, &maps.b[box], bar, b0 + 64, row + at, 0);
+        };
+        const int rows = kb == tl.kb - 1 ? tl.tail : kBlockK;
+        if (rank == 0) mbar_arrive_expect_tx_elect(&full[stage], 2 * boxes * rows * 128);
+        // (pieces start at multiples of 16 rows, and the swizzle's pattern at those of 8)
+        if (rows >= 16) copy(rows / 16 + 14, 0);
+        if (rows & 15) copy((rows & 15) - 1, rows & 48);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -865,13 +864,13 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[stage], phase, abort_flag, g.timeout_ns));
           if (!ok) break;
           int steps = 4;   // MMAs of 16 reduction rows; whole steps past the expert's end are left out
-          if (kb == blocks - 1 && tail < kBlockK) {
+          if (kb == blocks - 1 && tail % 16) {
             ok = __all_sync(0xFFFFFFFFu,
                             mbar_wait_bounded(&cleared[stage], (tails >> stage) & 1u, abort_flag, g.timeout_ns));
             if (!ok) break;
             tails ^= 1u << stage;
-            steps = (tail + 15) / 16;
           }
+          if (kb == blocks - 1) steps = (tail + 15) / 16;
           tc_fence_after();
           // (16 rows of 128 bytes down the boxes)
           const uint32_t a = base + stage * F::kStage;
@@ -905,48 +904,42 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
     }
   } else if (warp == kEpiWarps + 2) {
     // ------------------------------------------------------------------ clearing (even CTA)
-    // An expert's last rows: the rest of their last step of 16 is cleared in all
-    // four boxes (a row is 128 consecutive bytes of its box, and stays in its
-    // place under the swizzle).  A warp of its own does so while the MMAs before
-    // are issued: with the issuer clearing, uneven experts took 197 us instead of
-    // 193 (128 experts of 1536 x 2048, 256 rows each on average).  It clears both
-    // CTAs' boxes, so that all that orders it is in this CTA: an arrival from the
-    // other one would have to be a release at cluster scope, with which experts of
-    // up to 1360 rows took 231 us instead of 212 (217 with this CTA's boxes first:
-    // the other's take longer).
+    // Behind an expert's last rows the rest of their last step of 16 is cleared in
+    // all four boxes (a row is 128 consecutive bytes of its box, and stays in its
+    // place under the swizzle), while the rows themselves are on their way.  This
+    // CTA clears both CTAs' boxes, so that all that orders it is in this CTA: an
+    // arrival from the other one would have to be a release at cluster scope, with
+    // which experts of up to 1360 rows took 231 us instead of 212.
     int stage = 0;
-    uint32_t tails = 0;
-    int64_t blocks = 0;   // since the last wait, and their tiles: those without a tail are passed by
-    int tiles = 0;
+    uint32_t phase = 0;
     bool ok = true;
     for (bool more = rank == 0 && tl.first(g, t0); more && ok; more = tl.next(g, t_step)) {
-      if (tl.kb == 0) continue;
-      blocks += tl.kb;
-      ++tiles;
-      if (tl.tail < kBlockK) {
-        const int at = (stage + tl.kb - 1) % kStages;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&landed[at], (tails >> at) & 1u, abort_flag,
-                                                       tiles_limit(g, blocks, tiles)));
+      for (int kb = 0; kb < tl.kb; ++kb) {
+        // (of every block, as the producer does: a phase must not be passed by)
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, g.timeout_ns));
         if (!ok) break;
-        blocks = tiles = 0;
-        tails ^= 1u << at;
-        const int clear = ((tl.tail + 15) / 16 * 16 - tl.tail) * 8;   // 16-byte pieces of a box
-        uint8_t* first = smem + at * F::kStage + tl.tail * 128;
-        const uint32_t other = mapa(smem_u32(first), 1);
-        for (int i = lane; i < clear; i += 32)
+        if (kb == tl.kb - 1 && tl.tail % 16) {
+          const int clear = (16 - tl.tail % 16) * 8;   // 16-byte pieces of a box
+          uint8_t* first = smem + stage * F::kStage + tl.tail * 128;
+          const uint32_t other = mapa(smem_u32(first), 1);
+          for (int i = lane; i < clear; i += 32)
 #pragma unroll
-          for (int box = 0; box < 4; ++box) clear_remote16(other + box * kBoxBytes + i * 16);
-        for (int i = lane; i < clear; i += 32)
+            for (int box = 0; box < 4; ++box) clear_remote16(other + box * kBoxBytes + i * 16);
+          for (int i = lane; i < clear; i += 32)
 #pragma unroll
-          for (int box = 0; box < 4; ++box)
-            *reinterpret_cast<uint4*>(first + box * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
-        // ordered before the MMAs' reads of both CTAs' boxes
-        fence_proxy_async_cluster_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&cleared[at]);
-        __syncwarp();
+            for (int box = 0; box < 4; ++box)
+              *reinterpret_cast<uint4*>(first + box * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+          // ordered before the MMAs' reads of both CTAs' boxes
+          fence_proxy_async_cluster_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&cleared[stage]);
+          __syncwarp();
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      stage = (stage + tl.kb) % kStages;
     }
     if (!ok && lane == 0) {
       set_status(g.status, MOE_ERR_TIMEOUT);
@@ -972,7 +965,7 @@ __global__ void __launch_bounds__(Cfg<kWgrad>::kThreads, 1)
       more = tl.next(g, t_step);   // (its loads are on their way while this tile is waited for)
       if (any) {
         if (!__all_sync(0xFFFFFFFFu,
-                        mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, tiles_limit(g, kb, 1)))) {
+                        mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, tile_limit(g, kb)))) {
           set_status(g.status, MOE_ERR_TIMEOUT);
           *abort_flag = 1;
           break;
@@ -1314,9 +1307,9 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
     return no_rows(E, start, counts, status, stream);
   }
   WgradMaps m;
-  for (int i = 0; i < 4; ++i) {
-    if ((st = rows_map(&m.a[i], dy, rows, N, dy_ld, 16 * (i + 1))) != MOE_OK) return st;
-    if ((st = rows_map(&m.b[i], x, rows, C, x_ld, 16 * (i + 1))) != MOE_OK) return st;
+  for (int i = 0; i < kBoxes; ++i) {
+    if ((st = rows_map(&m.a[i], dy, rows, N, dy_ld, wgrad_box_rows(i))) != MOE_OK) return st;
+    if ((st = rows_map(&m.b[i], x, rows, C, x_ld, wgrad_box_rows(i))) != MOE_OK) return st;
   }
   const uint64_t d[3] = {static_cast<uint64_t>(C), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
   const uint64_t strides[2] = {C * size, static_cast<uint64_t>(N) * C * size};
