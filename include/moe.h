@@ -394,8 +394,9 @@ moe_status_t moe_unsort_tokens_backward(const void* dout, int64_t dout_ld, const
  * multiples of 8, E <= 1024, rows < 2^31 (MOE_ERR_UNSUPPORTED otherwise);
  * matrices 16-byte aligned (MOE_ERR_MISALIGNED).  status: device int32, not
  * cleared here, set where 0 to MOE_ERR_INVALID_ARG when an expert's numbers do
- * not fit the buffers (that expert is left out) or to MOE_ERR_TIMEOUT; the
- * workspace of moe_sort_plan can serve (moe_read_device_status reads it). */
+ * not fit the buffers (that expert is left out; reported with rows = 0 too) or
+ * to MOE_ERR_TIMEOUT; the workspace of moe_sort_plan can serve until the next
+ * plan clears it (moe_read_device_status reads it). */
 moe_status_t moe_expert_gemm(const void* x, int64_t x_ld, int64_t rows, const void* w, const int32_t* start,
                              const int32_t* counts, int32_t E, int64_t N, int64_t C, void* y, int64_t y_ld,
                              void* status, void* stream);

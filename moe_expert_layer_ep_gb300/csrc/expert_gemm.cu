@@ -48,10 +48,11 @@
 // 512, and 32 KB in that time is 63 B per clock, about what an SM gets from L2:
 // the two limits coincide, and lower tiles are held by the second (192 tokens:
 // 437 cycles for 384).  With all SMs busy the board's power cap then sets the
-// clock (1.3 - 1.7 GHz): 8 x 2048 rows of 4096 x 4096 take 286 us forward, 287 us
-// for the rows' gradient and 293 us for the weights' in the first milliseconds,
-// 330, 330 and 336 us (1667, 1666, 1638 TFLOP/s) when they run on at 1220 W; the
-// library's dense product of 16384 x 4096 x 4096 280 and 318 us.  Few rows per expert are bound by the weights' bytes (16 tokens on
+// clock (1.3 - 1.7 GHz): 8 x 2048 rows of 4096 x 4096 take 291 us forward, 290 us
+// for the rows' gradient and 299 us for the weights' in the first milliseconds,
+// 331, 331 and 345 us (1664, 1659, 1595 TFLOP/s) when they run on at 1250 W; the
+// library's dense product of 16384 x 4096 x 4096 281 and 318 us.  Few rows per
+// expert are bound by the weights' bytes (16 tokens on
 // 32 experts: 7.3 TB/s), 256 rows per expert nearly so (1536 x 2048 weights:
 // 6.1 - 6.6 TB/s), and the weights' gradient by what L2 moves, writes counting
 // twice (128 x 1536 x 2048, 256 rows each: 183 us; 133 us without the stores,
@@ -204,7 +205,8 @@ __device__ __forceinline__ void store_tile(uint8_t* tile, const CUtensorMap* map
 
 // 1 / (1 + exp(-x)) by the hardware's base-2 exponential and reciprocal, both
 // within 2 ulp: the epilogue's arithmetic is issue-bound (an IEEE quotient costs
-// as much as the rest), and the result is rounded to bf16.
+// as much as the rest), and the result is rounded to bf16.  0 below x = -87.3, where
+// it is less than 2^-126.
 __device__ __forceinline__ float sigmoid_fast(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
@@ -734,11 +736,10 @@ struct WgradTile {
 // Tensor maps of a gradient of the weights.  a: dy, b: x, in boxes of 64 columns
 // and wgrad_box_rows(i) rows, so that an expert's last rows are copied as they are,
 // in two pieces at most, and what is behind them can be cleared meanwhile.  In us,
-// 128 experts of 1536 x 2048 with 225 to 292 rows and with up to 1360, and for 16 of
-// 700: boxes of 16, 32, 48 and 64 rows, cleared once they have landed, 209, 212 and
-// 57; three pieces (1 - 8, 16, 32, 48 rows) 209, 214 and 55; so 201, 208 and 54; a
-// box of every height 196, 201 and 52, but forming 128 maps takes the host 5 us a
-// call more than four heights do, these 38 one.
+// 128 experts of 1536 x 2048 with 225 to 292 rows and with up to 1360, and 16 of
+// 700: boxes of 16, 32, 48 and 64 rows, cleared once they have landed, 205, 210 and
+// 56; so 196, 206 and 53; a box of every height 191, 199 and 51, but forming 128
+// maps takes the host 5 us a call more than four heights do, these 38 one.
 constexpr int kBoxes = 19;
 struct WgradMaps {
   CUtensorMap a[kBoxes], b[kBoxes], out;
