@@ -8,31 +8,32 @@
 //             + sum over j with id_j = e of w_j (dw_j - sum_i w_i dw_i)
 //   dx      = dz W + residual (bf16),   dW = dz^T x (fp32)
 //
-// Four kernels, and a fifth where dW's sums were split:
+// Three kernels, and a fourth where dW's sums were split:
 //   route_prepare_kernel assignments per expert and tokens that have one; W in fp16, each
 //                        expert's row times a power of two
 //   route_dz_kernel      a warp per token: dz in three bf16 planes whose sum it is (as
 //                        moe_router_prepare splits the weights) and, for dx, in fp16
 //                        times a power of two, without the weights' own; zeros behind the
 //                        experts up to a multiple of 64; the losses of eight tokens, which
-//                        router_dw_kernel adds
-//   router_dx_kernel     dz W on the tensor cores in fp16: 11 bits of each factor, so each
+//                        dW's part of the next kernel adds
+//   router_products_kernel  both products, dx on some of the CTA pairs and dW on the others:
+//     dx                 dz W on the tensor cores in fp16: 11 bits of each factor, so each
 //                        term is at most 2^-10 off, for a result that is stored with 8 bits
 //                        (over many terms the storing is what is left of the error: 1.66e-3
 //                        of the norm, 1.64e-3 with exact factors); three products of bf16
 //                        planes cost three times the MMAs (the whole call 132 us, so then 112)
-//   router_dw_kernel     dz^T x likewise: x is bf16, so three products per block are dz's
+//     dW                 dz^T x likewise: x is bf16, so three products per block are dz's
 //                        fp32 value times x
 //   router_dw_sum_kernel the parts of a split sum, in order
 //
-// router_dx_kernel.  A tile of 256 tokens x 256 columns on a CTA pair, tokens in lanes, so
+// dx.  A tile of 256 tokens x 256 columns on a CTA pair, tokens in lanes, so
 // that a thread's columns lie side by side in memory and its power of two is one number.
 //
 // What bounds it at 8192 x 7168 and 256 experts: the SM's epilogue and shared memory (a tile
 // takes 4900 cycles where its MMAs take 2070: operands, residual and result pass through
 // shared memory eight times over, 512 KB a tile).
 //
-// router_dw_kernel.  D = x^T dz, a tile of 256 columns of x by at most 128 experts on a
+// dW.  D = x^T dz, a tile of 256 columns of x by at most 128 experts on a
 // CTA pair, both operands MN-major (no transposed copies), the three planes' MMAs on one
 // copy of x: 40 KB per SM and 64 tokens for 768 cycles of MMAs.  Experts on the N side cost
 // what there are of them, up to a multiple of 32, and put x's columns into lanes, so that a
@@ -229,11 +230,10 @@ __global__ void __launch_bounds__(32 * kDzWarps, Q <= 2 ? 6 : Q == 4 ? 4 : 2) ro
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kDzWarps + warp;
   __shared__ float2 s_part[kDzWarps];
   __shared__ float s_row[kDzWarps][64 * Q];
+  pdl_wait();
   pdl_trigger();
   float2 part = make_float2(0.0f, 0.0f);
   if (t < g.T) {
-    // What the call is given is read while the counts are still made: the kernel that
-    // makes them lets this one start after it has waited for all work before.
     float z[2 * Q];
 #pragma unroll
     for (int i = 0; i < 2 * Q; ++i) {
@@ -261,7 +261,6 @@ __global__ void __launch_bounds__(32 * kDzWarps, Q <= 2 ? 6 : Q == 4 ? 4 : 2) ro
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 2 * Q; ++i) top = fmaxf(top, z[i]);
-    pdl_wait();
     if (there) {
       float f[2 * Q];
 #pragma unroll
@@ -359,7 +358,6 @@ __global__ void __launch_bounds__(32 * kDzWarps, Q <= 2 ? 6 : Q == 4 ? 4 : 2) ro
   }
   if (lane == 0) s_part[warp] = part;
   __syncthreads();
-  if (t >= g.T) pdl_wait();   // (a warp without a token)
   if (threadIdx.x == 0) {
     float2 sum = make_float2(0.0f, 0.0f);
     for (int w = 0; w < kDzWarps; ++w) {
@@ -390,15 +388,18 @@ constexpr int kDxSlots = 3;                      // chunks of an epilogue warp
 constexpr int kDxOffSlots = kDxStages * kDxStage;
 constexpr int kDxOffBars = kDxOffSlots + kEpiWarps * kDxSlots * kChunk;
 constexpr int kDxNumBars = 2 * kDxStages + 5 + kEpiWarps * kDxSlots;
-constexpr int kDxOffHolder = kDxOffBars + kDxNumBars * 8;
-constexpr int kDxSmem = kDxOffHolder + 16 + 1024;
-static_assert(kDxSmem <= 227 * 1024, "shared memory");
+// both parts' holder of the tensor memory's address and their abort flag; dW's part ends
+// before it (below)
+constexpr int kOffHolder = kDxOffBars + kDxNumBars * 8;
+constexpr int kSmem = kOffHolder + 16 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct DxMaps {
   CUtensorMap dz, w, res, out;
 };
 
 struct DxArgs {
+  int32_t pairs;           // CTA pairs that work on it
   int32_t Ep, e_blocks, t_tiles, k_tiles;
   int64_t T, K;
   const int32_t* row_exps;
@@ -428,51 +429,44 @@ __device__ __noinline__ void leave_copies_time() {
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    router_dx_kernel(const __grid_constant__ DxMaps maps, const __grid_constant__ DxArgs g) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kDxOffBars);
-  uint64_t* empty = full + kDxStages;
-  uint64_t* tfull = empty + kDxStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* done = tempty + 2;
-  uint64_t* arrived = done + 1;   // of each epilogue warp's chunks: the residual is there
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kDxOffHolder);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDxOffHolder + 4);
+// A part's barriers, by one thread.
+template <int kPartStages>
+__device__ __forceinline__ void init_bars(uint64_t* full, uint64_t* empty, uint64_t* tfull, uint64_t* tempty, uint64_t* done) {
+  for (int s = 0; s < kPartStages; ++s) {
+    mbar_init(&full[s], 1);     // (the even CTA's is used: its producer arrives, both CTAs' copies count)
+    mbar_init(&empty[s], 1);
+  }
+  for (int a = 0; a < 2; ++a) {
+    mbar_init(&tfull[a], 1);
+    mbar_init(&tempty[a], 2 * kEpiWarps);   // (the even CTA's: both CTAs' epilogue warps)
+  }
+  mbar_init(done, 1);
+}
+
+struct DxBars {
+  uint64_t full[kDxStages], empty[kDxStages], tfull[2], tempty[2], done;
+  uint64_t arrived[kEpiWarps * kDxSlots];   // of each epilogue warp's chunks: the residual is there
+};
+static_assert(sizeof(DxBars) == kDxNumBars * 8, "shared memory");
+
+__device__ __forceinline__ void dx_init(uint8_t* smem, const DxMaps& maps) {
+  DxBars* b = reinterpret_cast<DxBars*>(smem + kDxOffBars);
+  init_bars<kDxStages>(b->full, b->empty, b->tfull, b->tempty, &b->done);
+  for (int c = 0; c < kEpiWarps * kDxSlots; ++c) mbar_init(&b->arrived[c], 1);
+  prefetch_tensormap(&maps.dz);
+  prefetch_tensormap(&maps.w);
+  prefetch_tensormap(&maps.out);
+}
+
+// The work of CTA pair i0 of g.pairs.
+__device__ __forceinline__ void dx_part(uint8_t* smem, const DxMaps& maps, const DxArgs& g, int i0, uint32_t tmem) {
+  DxBars* bars = reinterpret_cast<DxBars*>(smem + kDxOffBars);
+  uint64_t *full = bars->full, *empty = bars->empty, *tfull = bars->tfull, *tempty = bars->tempty, *done = &bars->done;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffHolder + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kDxStages; ++s) {
-      mbar_init(&full[s], 1);     // (the even CTA's is used: its producer arrives, both CTAs' copies count)
-      mbar_init(&empty[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps);   // (the even CTA's: both CTAs' epilogue warps)
-    }
-    mbar_init(done, 1);
-    for (int c = 0; c < kEpiWarps * kDxSlots; ++c) mbar_init(&arrived[c], 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-    prefetch_tensormap(&maps.dz);
-    prefetch_tensormap(&maps.w);
-    prefetch_tensormap(&maps.out);
-  }
-  if (warp == 1) {
-    tmem_alloc_pair(holder, kTmemCols);
-    tmem_relinquish_pair();
-  }
-  pdl_wait();
-  pdl_trigger();
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = *holder;
   const int items = g.t_tiles * g.k_tiles;
-  const int i0 = blockIdx.x >> 1, i_step = gridDim.x >> 1;
+  const int i_step = g.pairs;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (both CTAs)
@@ -562,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // worked on.  (Loads to registers a tile ahead were waited for at the next barrier.)
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* slots = smem + kDxOffSlots + (warp - 2) * kDxSlots * kChunk;   // (128-byte rows, 128-byte swizzle)
-    arrived += (warp - 2) * kDxSlots;
+    uint64_t* arrived = bars->arrived + (warp - 2) * kDxSlots;
     const int row0 = static_cast<int>(rank) * 128 + quad * 32;   // of this warp in a tile
     int next_i = i0;   // the chunk to be copied in next, and its place
     int next_c = 0, next_slot = 0;
@@ -654,13 +648,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) bulk_wait_all();   // this warp's stores have completed
   }
-  // neither CTA leaves while the other's copies, MMAs or arrivals may reach it
-  __syncwarp();
-  cluster_sync();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc_pair(tmem, kTmemCols);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -674,15 +661,14 @@ constexpr int kStageBytes = 5 * kBoxBytes;       // x: two boxes; each plane of 
 constexpr int kStages = 5;
 constexpr int kOffBars = kStages * kStageBytes;
 constexpr int kNumBars = 2 * kStages + 5;
-constexpr int kOffHolder = kOffBars + kNumBars * 8;
-constexpr int kDwSmem = kOffHolder + 16 + 1024;
-static_assert(kDwSmem <= 227 * 1024, "shared memory");
+static_assert(kOffBars + kNumBars * 8 <= kOffHolder, "shared memory");
 
 struct DwMaps {
   CUtensorMap x, dz;
 };
 
 struct DwArgs {
+  int32_t pairs;           // CTA pairs that work on it
   int32_t E, Ep;
   int64_t K;
   int32_t segments;        // of 256 tokens
@@ -737,50 +723,27 @@ __device__ __noinline__ void sum_losses(const DwArgs& g, int lane) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    router_dw_kernel(const __grid_constant__ DwMaps maps, const __grid_constant__ DwArgs g) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBars);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* done = tempty + 2;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
+struct DwBars {
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], done;
+};
+static_assert(sizeof(DwBars) == kNumBars * 8, "shared memory");
+
+__device__ __forceinline__ void dw_init(uint8_t* smem, const DwMaps& maps) {
+  DwBars* b = reinterpret_cast<DwBars*>(smem + kOffBars);
+  init_bars<kStages>(b->full, b->empty, b->tfull, b->tempty, &b->done);
+  prefetch_tensormap(&maps.x);
+  prefetch_tensormap(&maps.dz);
+}
+
+// The work of CTA pair i0 of g.pairs.
+__device__ __forceinline__ void dw_part(uint8_t* smem, const DwMaps& maps, const DwArgs& g, int i0, uint32_t tmem) {
+  DwBars* bars = reinterpret_cast<DwBars*>(smem + kOffBars);
+  uint64_t *full = bars->full, *empty = bars->empty, *tfull = bars->tfull, *tempty = bars->tempty, *done = &bars->done;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffHolder + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);     // (the even CTA's is used: its producer arrives, both CTAs' copies count)
-      mbar_init(&empty[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kEpiWarps);   // (the even CTA's: both CTAs' epilogue warps)
-    }
-    mbar_init(done, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-    prefetch_tensormap(&maps.x);
-    prefetch_tensormap(&maps.dz);
-  }
-  if (warp == 1) {
-    tmem_alloc_pair(holder, kTmemCols);
-    tmem_relinquish_pair();
-  }
-  // This kernel does not read what the one before it (dx) writes: it may run beside
-  // it.  The one before that (dz) has completed, since dx lets this one start only
-  // after it has waited for dz; and this one does not end before dx has.
-  pdl_trigger();
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = *holder;
   const int items = g.k_tiles * g.e_tiles * g.parts;
-  const int i0 = blockIdx.x >> 1, i_step = gridDim.x >> 1;
+  const int i_step = g.pairs;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (both CTAs)
@@ -877,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int iter = 0;
     bool ok = true;
     // (in the last CTA, which has no more items than any other, while its first MMAs run)
-    if (g.losses && blockIdx.x == gridDim.x - 1 && warp == 2 + kEpiWarps - 1) sum_losses(g, lane);
+    if (g.losses && i0 == g.pairs - 1 && rank == 1 && warp == 2 + kEpiWarps - 1) sum_losses(g, lane);
     for (int i = i0; i < items && ok; i += i_step) {
       const DwItem it = dw_item(g, i);
       float run[64];   // of this lane's column of x: 64 experts' sums so far
@@ -919,7 +882,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (e0 + j < g.E) dst[j * g.K] = g.add ? dst[j * g.K] + run[j] : run[j];
     }
   }
+}
+
+// dx on the first pairs, dW on the others.  (In launches of their own that ran side by side
+// dW's read dz without having waited for it itself.)
+__global__ void __launch_bounds__(kThreads, 1)
+    router_products_kernel(const __grid_constant__ DxMaps dx_maps, const __grid_constant__ DxArgs dx,
+                           const __grid_constant__ DwMaps dw_maps, const __grid_constant__ DwArgs dw) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + kOffHolder);
+  const int warp = threadIdx.x >> 5, pair = static_cast<int>(blockIdx.x >> 1);
+  if (threadIdx.x == 0) {
+    if (pair < dx.pairs)
+      dx_init(smem, dx_maps);
+    else
+      dw_init(smem, dw_maps);
+    *reinterpret_cast<volatile int*>(holder + 1) = 0;   // the abort flag
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(holder, kTmemCols);
+    tmem_relinquish_pair();
+  }
   pdl_wait();
+  pdl_trigger();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  if (pair < dx.pairs)
+    dx_part(smem, dx_maps, dx, pair, tmem);
+  else
+    dw_part(smem, dw_maps, dw, pair - dx.pairs, tmem);
   // neither CTA leaves while the other's copies, MMAs or arrivals may reach it
   __syncwarp();
   cluster_sync();
@@ -951,6 +947,7 @@ __global__ void __launch_bounds__(256) router_dw_sum_kernel(const float4* parts,
 // ---------------------------------------------------------------------------
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t cuts(int64_t n, int64_t of) { return (n + of - 1) / of; }
+int32_t fewer(int32_t pairs, int64_t items) { return items < pairs ? static_cast<int32_t>(items) : pairs; }
 
 // dx and dW run side by side, each on its share of the 76 CTA pairs, dW's MMAs beside dx's
 // way through memory and fewer pairs without work at the end of both (4096 tokens, K = 2048,
@@ -1108,13 +1105,7 @@ moe_status_t moe_route_backward(const void* x_bf16, const void* w_planes, const 
   d.residual = residual != nullptr;
   d.status = status;
   d.timeout_ns = 2000000000ull;
-  static PerDevice known_dx;
-  int pairs = 0;
-  MOE_TRY(on_current_device(known_dx, &pairs, [](int* n) { return resident_pairs(router_dx_kernel, kThreads, kDxSmem, n); }));
-  if (pairs > at.shares.dx_pairs) pairs = at.shares.dx_pairs;
-  int64_t items = static_cast<int64_t>(d.t_tiles) * d.k_tiles;
-  MOE_TRY(launch_pdl_cluster(router_dx_kernel, dim3(2 * static_cast<unsigned>(items < pairs ? items : pairs)),
-                             dim3(kThreads), kDxSmem, s, 2, dx_maps, d));
+  d.pairs = fewer(at.shares.dx_pairs, static_cast<int64_t>(d.t_tiles) * d.k_tiles);
 
   DwArgs g;
   memset(&g, 0, sizeof(g));
@@ -1133,12 +1124,12 @@ moe_status_t moe_route_backward(const void* x_bf16, const void* w_planes, const 
   g.losses = losses;
   g.status = status;
   g.timeout_ns = 2000000000ull;
+  g.pairs = fewer(at.shares.dw_pairs, static_cast<int64_t>(g.k_tiles) * g.e_tiles * g.parts);
   static PerDevice known;
-  MOE_TRY(on_current_device(known, &pairs, [](int* n) { return resident_pairs(router_dw_kernel, kThreads, kDwSmem, n); }));
-  if (pairs > at.shares.dw_pairs) pairs = at.shares.dw_pairs;
-  items = static_cast<int64_t>(g.k_tiles) * g.e_tiles * g.parts;
-  MOE_TRY(launch_pdl_cluster(router_dw_kernel, dim3(2 * static_cast<unsigned>(items < pairs ? items : pairs)),
-                             dim3(kThreads), kDwSmem, s, 2, maps, g));
+  int resident = 0;   // (no pair waits for another: more than fit run one after another)
+  MOE_TRY(on_current_device(known, &resident, [](int* n) { return resident_pairs(router_products_kernel, kThreads, kSmem, n); }));
+  MOE_TRY(launch_pdl_cluster(router_products_kernel, dim3(2 * static_cast<unsigned>(d.pairs + g.pairs)), dim3(kThreads), kSmem,
+                             s, 2, dx_maps, d, maps, g));
   if (g.parts > 1) {
     const int64_t n4 = static_cast<int64_t>(E) * K / 4;
     MOE_TRY(launch_pdl(router_dw_sum_kernel, dim3(static_cast<unsigned>(cuts(n4, 256))), dim3(256), 0, s,
