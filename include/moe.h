@@ -464,16 +464,26 @@ moe_status_t moe_expert_bias_grad(const void* dy, int64_t dy_ld, int64_t rows, c
                                   void* status, void* stream);
 
 /* The router's gradient, and that of its two losses.  x, w_planes, logits, topk_ids
- * and topk_weights as moe_route took and gave them, but ids may be set to -1 (an
- * assignment that was dropped); dweights fp32 [T, topk] as
- * moe_unsort_tokens_backward gives them.  A token whose ids are all -1 is padding:
- * nothing of it counts, whatever its logits and weights hold (x must be finite).
- * With p = softmax of a token's logits, and means over the n other tokens:
- *   losses[0] = E_global * sum over e of f_e P_e    f_e = assignments of e / (n topk)
+ * and topk_weights as moe_route took and gave them; dweights fp32 [T, topk] as
+ * moe_unsort_tokens_backward gives them.  Assignments that were dropped (left out of
+ * their token's sum) are marked by what became of the weights:
+ *   weights as moe_route gave them, the softmax over all topk selected:
+ *       moe_route_backward_kept with the ids as moe_route gave them and kept uint8
+ *       [T, topk], 0 for a dropped assignment (on a rank with all experts: src2dst >= 0
+ *       of a moe_sort_plan that was given -1 for it); its dw_j counts as 0, whatever is
+ *       there, but the softmax's derivative reaches its logit.  NULL: all are kept
+ *   weights made the softmax over those that are left:
+ *       its id -1; nothing of it counts, whatever its weight and dw_j hold.  (With the
+ *       weights over all topk this would not be their gradient: it lacks the term
+ *       -w_j * sum over i of w_i dw_i of the dropped one's logit.)
+ * A token whose ids are all -1 is padding: nothing of it counts, whatever its logits
+ * and weights hold (x must be finite).  With p = softmax of a token's logits, and
+ * means over the n other tokens:
+ *   losses[0] = E_global * sum over e of f_e P_e    f_e = kept assignments of e / (n topk)
  *                                                   P_e = mean of p_e
  *   losses[1] = mean of the logits' logsumexp, squared
  *   dz = gradient of balance * losses[0] + zloss * losses[1] (f a constant), and for
- *        every kept assignment w_j (dw_j - sum over kept i of w_i dw_i) to its logit
+ *        every id w_j (dw_j - sum over i of w_i dw_i) to its logit
  *   dx bf16 [T, K] = dz W + residual (bf16 [T, K], may be dx; or NULL)
  *   dw fp32 [E_global, K] = dz^T x; accumulate != 0: added to dw
  * dlogits (dz, fp32 [T, E_global]) and losses (fp32 [2]) may be NULL.  dz and dW's
@@ -494,6 +504,12 @@ moe_status_t moe_route_backward(const void* x_bf16, const void* w_planes, const 
                                 int32_t E_global, int32_t topk, double balance, double zloss, const void* residual,
                                 void* dx_bf16, float* dw, int32_t accumulate, float* dlogits, float* losses, void* ws,
                                 int64_t ws_bytes, void* stream);
+moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, const float* logits,
+                                     const int32_t* topk_ids, const float* topk_weights, const float* dweights,
+                                     const uint8_t* kept, int64_t T, int64_t K, int32_t E_global, int32_t topk,
+                                     double balance, double zloss, const void* residual, void* dx_bf16, float* dw,
+                                     int32_t accumulate, float* dlogits, float* losses, void* ws, int64_t ws_bytes,
+                                     void* stream);
 
 /* One AdamW step over many tensors.  Per element, in fp32:
  *   g' = grad_scale * g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2

@@ -132,6 +132,8 @@ def _load():
         "moe_route_backward_workspace_size": (I64, [I64, I64, I32]),
         "moe_route_backward": (I32, [VP, VP, VP, VP, VP, VP, I64, I64, I32, I32, F64, F64, VP, VP, VP, I32, VP, VP, VP, I64,
                                      VP]),
+        "moe_route_backward_kept": (I32, [VP, VP, VP, VP, VP, VP, VP, I64, I64, I32, I32, F64, F64, VP, VP, VP, I32, VP, VP, VP,
+                                          I64, VP]),
         "moe_adamw_create": (I32, [P(MoeAdamwTensor), I32, P(VP)]),
         "moe_adamw_destroy": (None, [VP]),
         "moe_adamw_launches": (I32, [VP]),
@@ -156,7 +158,7 @@ EXPORTED = ("moe_compact_all_tokens", "moe_choose_layout", "moe_ctx_create", "mo
             "moe_expert_gemm_dgrad", "moe_expert_gemm_dgrad_swiglu", "moe_expert_gemm_wgrad", "moe_adamw_create", "moe_adamw_destroy",
             "moe_adamw_launches", "moe_adamw_step", "moe_expert_gemm_act", "moe_expert_gemm_glu",
             "moe_expert_gemm_dgrad_act", "moe_expert_gemm_dgrad_glu", "moe_expert_bias_grad",
-            "moe_route_backward_workspace_size", "moe_route_backward")
+            "moe_route_backward_workspace_size", "moe_route_backward", "moe_route_backward_kept")
 
 
 def _check(code, what):
@@ -803,12 +805,14 @@ def moe_route_backward_workspace_size(T, K, E):
 
 
 def moe_route_backward(x, w_planes, logits, topk_ids, topk_weights, dweights, balance=0.0, zloss=0.0, residual=None,
-                       dx=None, dw=None, accumulate=False, dlogits=None, losses=None, ws=None, stream=None):
+                       dx=None, dw=None, accumulate=False, dlogits=None, losses=None, ws=None, stream=None, kept=None):
     """Gradient of moe_route and of its losses: x bf16 [T, K], w_planes bf16 [3, E, K], logits fp32 [T, E], topk_ids
     int32, topk_weights and dweights fp32 [T, k] -> (dx bf16 [T, K], dw fp32 [E, K], losses fp32 [2]: the load balance
     and the mean squared logsumexp, of which balance and zloss are the factors in the total loss); see include/moe.h.
     residual: bf16 [T, K] added to dx (may be dx); accumulate: dw is added to; dlogits: fp32 [T, E], written if given.
-    ws: uint8 device scratch (allocated here if None) that begins with the status word."""
+    ws: uint8 device scratch (allocated here if None) that begins with the status word.  kept: bool or uint8 [T, k], 0 for
+    an assignment that was dropped although the weights are still those of all k; its id stays.  (An id of -1 instead
+    means that the weights are the softmax over the others.)"""
     if x.dim() != 2 or w_planes.dim() != 3 or topk_ids.dim() != 2:
         raise ValueError("x and topk_ids must be matrices, w_planes [3, E, K]")
     (T, K), E, topk = x.shape, w_planes.shape[1], topk_ids.shape[1]
@@ -820,9 +824,14 @@ def moe_route_backward(x, w_planes, logits, topk_ids, topk_weights, dweights, ba
     _require_cuda("dweights", dweights, torch.float32, T * topk)
     if residual is not None:
         _require_cuda("residual", residual, torch.bfloat16, T * K)
+    if kept is not None:
+        _require_cuda("kept", kept, None, T * topk)
+        if kept.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"kept must be bool or uint8, got {kept.dtype}")
     if accumulate and dw is None:
         raise ValueError("accumulate needs a dw to add to")
-    _on_current_device(x, w_planes, logits, topk_ids, topk_weights, dweights, residual, dx, dw, dlogits, losses, ws)
+    _on_current_device(x, w_planes, logits, topk_ids, topk_weights, dweights, residual, dx, dw, dlogits, losses, ws,
+                       kept)
     if dx is None:
         dx = _empty((T, K), torch.bfloat16, x, stream)
     if dw is None:
@@ -837,10 +846,10 @@ def moe_route_backward(x, w_planes, logits, topk_ids, topk_weights, dweights, ba
         _require_cuda("dlogits", dlogits, torch.float32, T * E)
     _require_cuda("losses", losses, torch.float32, 2)
     _require_cuda("ws", ws, torch.uint8)
-    _check(_lib.moe_route_backward(_ptr(x), _ptr(w_planes), _ptr(logits), _ptr(topk_ids), _ptr(topk_weights), _ptr(dweights),
-                                   T, K, E, topk, balance, zloss, _ptr(residual), _ptr(dx), _ptr(dw), accumulate,
-                                   _ptr(dlogits), _ptr(losses), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_route_backward")
+    _check(_lib.moe_route_backward_kept(_ptr(x), _ptr(w_planes), _ptr(logits), _ptr(topk_ids), _ptr(topk_weights),
+                                        _ptr(dweights), _ptr(kept), T, K, E, topk, balance, zloss, _ptr(residual), _ptr(dx),
+                                        _ptr(dw), accumulate, _ptr(dlogits), _ptr(losses), _ptr(ws), ws.numel(),
+                                        _stream(stream)), "moe_route_backward")
     return dx, dw, losses
 
 

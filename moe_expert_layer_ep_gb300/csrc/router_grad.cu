@@ -6,6 +6,8 @@
 //             f_e = assignments of e / (n k),  P_e = mean of p_e      have an expert)
 //   dz_e    = cb (E / n) p_e (f_e - sum_i f_i p_i) + cz (2 / n) l p_e
 //             + sum over j with id_j = e of w_j (dw_j - sum_i w_i dw_i)
+//             (an assignment that was dropped with its id kept: its dw is 0 and f_e does
+//             not count it, but its weight took part in the softmax)
 //   dx      = dz W + residual (bf16),   dW = dz^T x (fp32)
 //
 // Three kernels, and a fourth where dW's sums were split:
@@ -74,6 +76,7 @@ __device__ __forceinline__ int read_cluster(const int* p, int rank) {
 
 struct PrepareArgs {
   const int32_t* ids;      // [T, topk]
+  const uint8_t* kept;     // [T, topk] or null: all
   int64_t T;
   int32_t topk, E;
   int32_t* counts;
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kPrepareThreads, 2) route_prepare_kernel(const
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (id[j] >= 0 && id[j] < g.E) {
-          atomicAdd(&hist[id[j]], 1);
+          if (!g.kept || g.kept[t * g.topk + j0 + j]) atomicAdd(&hist[id[j]], 1);
           any = true;
         } else if (id[j] != -1) {
           bad = 1;
@@ -192,6 +195,7 @@ struct DzArgs {
   const int32_t* ids;
   const float* weights;
   const float* dweights;
+  const uint8_t* kept;     // [T, topk] or null: all
   int64_t T;
   int32_t E, Ep, topk;     // Ep: E up to a multiple of 64
   float balance, zloss;
@@ -249,12 +253,12 @@ __global__ void __launch_bounds__(32 * kDzWarps, Q <= 2 ? 6 : Q == 4 ? 4 : 2) ro
       const bool there = j < g.topk;
       id[h] = there ? g.ids[t * g.topk + j] : -1;
       wt[h] = there ? g.weights[t * g.topk + j] : 0.0f;
-      dw[h] = there ? g.dweights[t * g.topk + j] : 0.0f;
+      dw[h] = there && (!g.kept || g.kept[t * g.topk + j]) ? g.dweights[t * g.topk + j] : 0.0f;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (id[h] >= 0 && id[h] < g.E) continue;
-      id[h] = -1;   // dropped: whatever its weights are
+      id[h] = -1;   // no assignment: whatever its weights are
       wt[h] = dw[h] = 0.0f;
     }
     const bool there = __any_sync(kAll, id[0] >= 0 || id[1] >= 0);   // else padding: its logits may be anything
@@ -1042,6 +1046,16 @@ moe_status_t moe_route_backward(const void* x_bf16, const void* w_planes, const 
                                 int32_t E_global, int32_t topk, double balance, double zloss, const void* residual,
                                 void* dx_bf16, float* dw, int32_t accumulate, float* dlogits, float* losses, void* ws,
                                 int64_t ws_bytes, void* stream) {
+  return moe_route_backward_kept(x_bf16, w_planes, logits, topk_ids, topk_weights, dweights, nullptr, T, K, E_global, topk,
+                                 balance, zloss, residual, dx_bf16, dw, accumulate, dlogits, losses, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, const float* logits,
+                                     const int32_t* topk_ids, const float* topk_weights, const float* dweights,
+                                     const uint8_t* kept, int64_t T, int64_t K, int32_t E_global, int32_t topk,
+                                     double balance, double zloss, const void* residual, void* dx_bf16, float* dw,
+                                     int32_t accumulate, float* dlogits, float* losses, void* ws, int64_t ws_bytes,
+                                     void* stream) {
   const int32_t E = E_global;
   if (T < 0 || K <= 0 || E <= 0 || topk <= 0) return MOE_ERR_INVALID_ARG;
   if (K % 128 || K > (int64_t(1) << 30) || E > kMaxRouterExperts || topk > kMaxTopk || topk > E || T > (int64_t(1) << 30) ||
@@ -1085,11 +1099,11 @@ moe_status_t moe_route_backward(const void* x_bf16, const void* w_planes, const 
 
   int32_t* counts = reinterpret_cast<int32_t*>(base + at.counts);
   int32_t* tokens = reinterpret_cast<int32_t*>(base + at.tokens);
-  const PrepareArgs prepare = {topk_ids, T, topk, E, counts, tokens, status, static_cast<const uint4*>(w_planes), K / 8,
+  const PrepareArgs prepare = {topk_ids, kept, T, topk, E, counts, tokens, status, static_cast<const uint4*>(w_planes), K / 8,
                                reinterpret_cast<uint4*>(w_half), exps};
   MOE_TRY(launch_pdl_cluster(route_prepare_kernel, dim3(static_cast<unsigned>(kCountCtas + up(E, kCountCtas))),
                              dim3(kPrepareThreads), 0, s, kCountCtas, prepare));
-  DzArgs z = {logits, topk_ids, topk_weights, dweights, T, E, Ep, topk, static_cast<float>(balance),
+  DzArgs z = {logits, topk_ids, topk_weights, dweights, kept, T, E, Ep, topk, static_cast<float>(balance),
               static_cast<float>(zloss), counts, tokens, exps, planes, half, row_exps, dlogits, reinterpret_cast<float2*>(base + at.parts)};
   MOE_TRY((E <= 64 ? launch_dz<1> : E <= 128 ? launch_dz<2> : E <= 256 ? launch_dz<4> : E <= 512 ? launch_dz<8>
                                                                                             : launch_dz<16>)(z, s));

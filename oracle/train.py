@@ -131,15 +131,16 @@ def expert_bias_grad(dy, start, counts):
 
 
 # ---------------------------------------------------------------- router
-def route_losses(logits, ids):
-    """(balance, size): E sum_e f_e P_e, f_e the share of the assignments that went to e and P_e the mean probability
-    of e, and the mean square of the logits' logsumexp; means over the tokens that have an id."""
+def route_losses(logits, ids, kept=None):
+    """(balance, size): E sum_e f_e P_e, f_e the share of the assignments that went to e (those that were kept) and P_e
+    the mean probability of e, and the mean square of the logits' logsumexp; means over the tokens that have an id."""
     ids = np.asarray(ids)
+    kept = ids >= 0 if kept is None else (ids >= 0) & np.asarray(kept, dtype=bool)
     T, E = logits.shape
     there = (ids >= 0).any(axis=1)
     n = max(1, int(there.sum()))
     f = np.zeros(E)
-    for e in ids[ids >= 0]:
+    for e in ids[kept]:
         f[e] += 1.0 / (n * ids.shape[1])
     top = logits.max(axis=1, keepdims=True)
     lse = top[:, 0] + np.log(np.exp(logits - top).sum(axis=1))
@@ -147,15 +148,17 @@ def route_losses(logits, ids):
     return E * float((f * p[there].sum(axis=0)).sum()) / n, float((lse[there] ** 2).sum()) / n
 
 
-def route_backward(logits, ids, weights, dweights, balance, zloss):
-    """Gradient to the logits of balance * the first loss + zloss * the second + sum(dweights * weights)."""
+def route_backward(logits, ids, weights, dweights, balance, zloss, kept=None):
+    """Gradient to the logits of balance * the first loss + zloss * the second + sum(dweights * weights), weights the
+    softmax over a token's ids that are not -1; with kept, the sum runs over the kept assignments alone."""
     ids = np.asarray(ids)
+    kept = ids >= 0 if kept is None else (ids >= 0) & np.asarray(kept, dtype=bool)
     T, E = logits.shape
     k = ids.shape[1]
     there = (ids >= 0).any(axis=1)
     n = max(1, int(there.sum()))
     f = np.zeros(E)
-    for e in ids[ids >= 0]:
+    for e in ids[kept]:
         f[e] += 1.0 / (n * k)
     dz = np.zeros((T, E))
     for t in range(T):
@@ -165,10 +168,10 @@ def route_backward(logits, ids, weights, dweights, balance, zloss):
         lse = z.max() + math.log(np.exp(z - z.max()).sum())
         p = np.exp(z - lse)
         dz[t] = balance * E / n * p * (f - (f * p).sum()) + zloss * 2.0 * lse / n * p
-        kept = [j for j in range(k) if ids[t, j] >= 0]
-        mean = sum(weights[t, j] * dweights[t, j] for j in kept)
-        for j in kept:
-            dz[t, ids[t, j]] += weights[t, j] * (dweights[t, j] - mean)
+        mean = sum(weights[t, j] * dweights[t, j] for j in range(k) if kept[t, j])
+        for j in range(k):
+            if ids[t, j] >= 0:
+                dz[t, ids[t, j]] += weights[t, j] * ((dweights[t, j] if kept[t, j] else 0.0) - mean)
     return dz
 
 
