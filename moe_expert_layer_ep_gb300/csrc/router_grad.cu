@@ -11,11 +11,13 @@
 //   dx      = dz W + residual (bf16),   dW = dz^T x (fp32)
 //
 // Three kernels, and a fourth where dW's sums were split:
-//   route_prepare_kernel assignments per expert and tokens that have one; W in fp16, each
-//                        expert's row times a power of two
+//   route_prepare_kernel assignments per expert and tokens that have one; W in fp16, less the
+//                        mean row m of four experts where that makes an expert's row clearly
+//                        smaller, each expert's row times a power of two
 //   route_dz_kernel      a warp per token: dz in three bf16 planes whose sum it is (as
 //                        moe_router_prepare splits the weights) and, for dx, in fp16
-//                        times a power of two, without the weights' own; zeros behind the
+//                        times a power of two, without the weights' own; its sum over the
+//                        experts whose rows are less m; zeros behind the
 //                        experts up to a multiple of 64; the losses of eight tokens, which
 //                        dW's part of the next kernel adds
 //   router_products_kernel  both products, dx on some of the CTA pairs and dW on the others:
@@ -23,7 +25,10 @@
 //                        term is at most 2^-10 off, for a result that is stored with 8 bits
 //                        (over many terms the storing is what is left of the error: 1.66e-3
 //                        of the norm, 1.64e-3 with exact factors); three products of bf16
-//                        planes cost three times the MMAs (the whole call 132 us, so then 112)
+//                        planes cost three times the MMAs (the whole call 132 us, so then 112).
+//                        A dz of softmaxes sums to 0, so what the rows of W have in common
+//                        cancels, and rounded factors would not (a common row 32 times the
+//                        rest: 9.7e-3): hence the rows less m, and dz's sum times m in fp32
 //     dW                 dz^T x likewise: x is bf16, so three products per block are dz's
 //                        fp32 value times x
 //   router_dw_sum_kernel the parts of a split sum, in order
@@ -62,16 +67,45 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 // ---------------------------------------------------------------------------
 constexpr int kPrepareThreads = 512;
 constexpr int kCountCtas = 8;
+constexpr int kMeanOf = 4;       // experts, evenly spread, whose mean row is taken
+// An expert's row is taken less the mean row where the sum of its sizes becomes smaller
+// than this share of what it was: rows that have nothing in common, whose mean is an accident
+// of the drawing, stay as they are, and so does an expert beside another of much larger
+// weights, whose mean would only be put into its row.  (Any row near the mean of all would
+// do, since what is taken off is put back: the mean of four leaves rows 1.12 times as large
+// as that of all, and each CTA forms it for itself, while the assignments are counted: of
+// eight, 1.06 times, 2.7 us more at 256 experts of 7168; of all, by a kernel before, 4 to 7.)
+constexpr float kCentred = 0.7f;
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }   // |e| <= 126
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
 __device__ __forceinline__ int read_cluster(const int* p, int rank) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa(smem_u32(p), rank)) : "memory");
   return static_cast<int>(v);
+}
+
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = unpack_bf16x2(x[j]);
+    v[2 * j] = p.x;
+    v[2 * j + 1] = p.y;
+  }
 }
 
 struct PrepareArgs {
@@ -84,44 +118,91 @@ struct PrepareArgs {
   int32_t* status;
   const uint4* planes;     // W [3][E][K]
   int64_t row8;            // K / 8
+  float* mean;             // [K]
   uint4* half;             // [E][K]
-  int32_t* exps;           // [E]
+  int32_t* exps;           // [E] the power of two, and 2^16 where the row is less the mean
 };
 
-// Row e of W times 2^exps[e] in fp16, its largest value in [2^14, 2^15) (exps within
-// +-126), from its first two planes.
+// What exps holds.
+__device__ __forceinline__ int exp_of(int32_t w) { return static_cast<int16_t>(w); }
+__device__ __forceinline__ bool is_centred(int32_t w) { return (w >> 16 & 1) != 0; }
+
+// Row e of W, or what is left of it without the mean row, times 2^exp in fp16, its largest
+// value in [2^14, 2^15) (exp within +-126).
 __device__ __forceinline__ void half_row(const PrepareArgs& g, int e) {
-  __shared__ float s_max[kPrepareThreads / 32];
+  __shared__ float4 s_part[kPrepareThreads / 32];
   const uint4* hi = g.planes + e * g.row8;
   const uint4* mid = hi + g.E * g.row8;
-  float most = 0.0f;
-  for (int64_t i = threadIdx.x; i < g.row8; i += kPrepareThreads) {
-    const uint4 a = hi[i], b = mid[i];
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  const uint4* lo = mid + g.E * g.row8;
+  const auto load = [&](const uint4* plane, int64_t i, float (&v)[8]) { unpack8(plane[i], v); };
+  const int of = min(kMeanOf, g.E);
+  const auto load_mean = [&](int64_t i, float (&v)[8]) {   // of the first planes
+    uint4 w[kMeanOf];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = unpack_bf16x2(x[j]), q = unpack_bf16x2(y[j]);
-      most = fmaxf(most, fmaxf(fabsf(p.x + q.x), fabsf(p.y + q.y)));
+    for (int n = 0; n < kMeanOf; ++n) w[n] = n < of ? g.planes[n * g.E / of * g.row8 + i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kMeanOf; ++n) {
+      float a[8];
+      unpack8(w[n], a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += a[j];
+    }
+    const float share = 1.0f / static_cast<float>(of);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= share;
+  };
+  float4 seen = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // largest and sum, as it is; largest and sum, without the mean
+  for (int64_t i = threadIdx.x; i < g.row8; i += kPrepareThreads) {
+    float a[8], b[8], m[8];
+    load(hi, i, a);
+    load(mid, i, b);
+    load_mean(i, m);
+    if (e == 0) {
+      float4* mean = reinterpret_cast<float4*>(g.mean) + 2 * i;
+      mean[0] = make_float4(m[0], m[1], m[2], m[3]);
+      mean[1] = make_float4(m[4], m[5], m[6], m[7]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float w = a[j] + b[j], c = fabsf(w - m[j]);
+      seen.x = fmaxf(seen.x, fabsf(w));
+      seen.y += fabsf(w);
+      seen.z = fmaxf(seen.z, c);
+      seen.w += c;
     }
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = most;
+  seen = make_float4(warp_max(seen.x), warp_sum(seen.y), warp_max(seen.z), warp_sum(seen.w));
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = seen;
   __syncthreads();
+  seen = s_part[0];
 #pragma unroll
-  for (int w = 0; w < kPrepareThreads / 32; ++w) most = fmaxf(most, s_max[w]);
+  for (int w = 1; w < kPrepareThreads / 32; ++w) {
+    const float4 p = s_part[w];
+    seen = make_float4(fmaxf(seen.x, p.x), seen.y + p.y, fmaxf(seen.z, p.z), seen.w + p.w);
+  }
+  const bool centred = seen.w < kCentred * seen.y;
+  const float most = centred ? seen.z : seen.x;
   const int exp = most > 0.0f ? max(-126, min(126, 141 - static_cast<int>(__float_as_uint(most) >> 23))) : 0;
   const float scale = pow2(exp);
-  if (threadIdx.x == 0) g.exps[e] = exp;
+  if (threadIdx.x == 0) g.exps[e] = (exp & 0xFFFF) | (centred ? 1 << 16 : 0);
   for (int64_t i = threadIdx.x; i < g.row8; i += kPrepareThreads) {
-    const uint4 a = hi[i], b = mid[i];
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float a[8], b[8];
+    load(hi, i, a);
+    load(mid, i, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] += b[j];
+    if (centred) {   // (the last plane too: it is 2^-17 of what was common)
+      float m[8];
+      load(lo, i, b);
+      load_mean(i, m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = a[j] + b[j] - m[j];
+    }
     uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = unpack_bf16x2(x[j]), q = unpack_bf16x2(y[j]);
-      o[j] = pack_half2((p.x + q.x) * scale, (p.y + q.y) * scale);
-    }
+    for (int j = 0; j < 4; ++j) o[j] = pack_half2(a[2 * j] * scale, a[2 * j + 1] * scale);
     g.half[e * g.row8 + i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
@@ -201,24 +282,14 @@ struct DzArgs {
   float balance, zloss;
   const int32_t* counts;
   const int32_t* tokens;
-  const int32_t* exps;     // [E] of the weights' fp16
+  const int32_t* exps;     // [E] of the weights' fp16 (PrepareArgs)
   uint16_t* planes;        // [T][3][Ep]
   uint16_t* half;          // [T][Ep] dz 2^-exps, times a power of two of the row, in fp16
-  int32_t* row_exps;       // [T] what dx of the row is multiplied by, 2 to its power
+  int2* rows;              // [T] 2 to the first's power: what the row's product is multiplied by;
+                           // the second, a float: dz's sum over the experts whose rows are less the mean
   float* dlogits;          // [T, E] or null
   float2* parts;           // [gridDim.x] sums of a CTA's tokens
 };
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
 
 // exp(x) by the hardware's base-2 exponential, 2 ulp and x's rounding; 0 below -87.3.
 __device__ __forceinline__ float exp_fast(float x) {
@@ -325,14 +396,20 @@ __global__ void __launch_bounds__(32 * kDzWarps, Q <= 2 ? 6 : Q == 4 ? 4 : 2) ro
     // largest of it to at least 2^14, in two factors with W's between them (each product
     // in fp32's range, or nothing beside the largest)
     int we[2 * Q], most = -1000;
+    float centred = 0.0f;
+    bool any = false;
 #pragma unroll
     for (int i = 0; i < 2 * Q; ++i) {
       const int e = 64 * (i >> 1) + 2 * lane + (i & 1);
-      we[i] = e < g.E ? g.exps[e] : 0;
+      const int32_t word = e < g.E ? g.exps[e] : 0;
+      we[i] = exp_of(word);
+      if (is_centred(word)) centred += z[i];
+      any |= is_centred(word);
       if (z[i] != 0.0f) most = max(most, static_cast<int>((__float_as_uint(z[i]) >> 23) & 255u) - 127 - we[i]);
     }
     const int up_by = min(14 - __reduce_max_sync(kAll, most), 252);
-    if (lane == 0) g.row_exps[t] = -up_by;
+    if (__any_sync(kAll, any)) centred = warp_sum(centred);
+    if (lane == 0) g.rows[t] = make_int2(-up_by, __float_as_int(centred));
     const float up0 = pow2(up_by / 2), up1 = pow2(up_by - up_by / 2);
     uint32_t* half = reinterpret_cast<uint32_t*>(g.half + t * g.Ep);
 #pragma unroll
@@ -406,7 +483,10 @@ struct DxArgs {
   int32_t pairs;           // CTA pairs that work on it
   int32_t Ep, e_blocks, t_tiles, k_tiles;
   int64_t T, K;
-  const int32_t* row_exps;
+  const int2* rows;        // [T] (DzArgs)
+  const int32_t* exps;     // [E] (PrepareArgs)
+  const float* mean;       // [K]
+  int32_t E;
   int32_t residual;
   int32_t* status;
   uint64_t timeout_ns;
@@ -460,6 +540,135 @@ __device__ __forceinline__ void dx_init(uint8_t* smem, const DxMaps& maps) {
   prefetch_tensormap(&maps.dz);
   prefetch_tensormap(&maps.w);
   prefetch_tensormap(&maps.out);
+}
+
+// kCentredRows: some expert's row is less the mean, and dz's sums times the mean are added.
+template <bool kCentredRows>
+__device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, const DxArgs& g, int i0, uint32_t tmem) {
+  DxBars* bars = reinterpret_cast<DxBars*>(smem + kDxOffBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffHolder + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  uint64_t *tfull = bars->tfull, *tempty = bars->tempty;
+  const int items = g.t_tiles * g.k_tiles, i_step = g.pairs;
+  // A lane holds a token; a warp takes half of the tile's columns, 64 at a time:
+  // whole lines of memory.  The residual is copied to where the result is formed and
+  // copied out from, in three places in turn: two chunks are on their way while one is
+  // worked on.  (Loads to registers a tile ahead were waited for at the next barrier.)
+  const int quad = warp & 3, half = (warp - 2) >> 2;
+  uint8_t* slots = smem + kDxOffSlots + (warp - 2) * kDxSlots * kChunk;   // (128-byte rows, 128-byte swizzle)
+  uint64_t* arrived = bars->arrived + (warp - 2) * kDxSlots;
+  const int row0 = static_cast<int>(rank) * 128 + quad * 32;   // of this warp in a tile
+  int next_i = i0;   // the chunk to be copied in next, and its place
+  int next_c = 0, next_slot = 0;
+  const auto copy_in = [&]() {
+    if (!g.residual || next_i >= items) return;
+    const DxItem it = dx_item(g, next_i);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&arrived[next_slot], kChunk);
+      tma_load_3d(slots + next_slot * kChunk, &maps.res, &arrived[next_slot], it.k0 + half * (it.n / 2) + next_c * 64,
+                  it.t0 + row0, 0);
+    }
+    next_slot = next_slot == kDxSlots - 1 ? 0 : next_slot + 1;
+    if (++next_c == it.n / 128) {
+      next_c = 0;
+      next_i += i_step;
+    }
+  };
+  for (int c = 0; c < kDxSlots; ++c) copy_in();
+  int slot = 0;
+  bool first = true;
+  int iter = 0;
+  bool ok = true;
+  uint32_t phases = 0;   // the places' parities
+  for (int i = i0; i < items && ok; i += i_step, ++iter) {
+    const DxItem it = dx_item(g, i);
+    const int acc = iter & 1;
+    // this lane's token: its power of two, in two factors that are numbers of their own
+    const int2 of = it.t0 + row0 + lane < g.T ? g.rows[it.t0 + row0 + lane] : make_int2(0, 0);
+    const int exp = of.x;
+    const float down0 = pow2(exp / 2), down1 = pow2(exp - exp / 2), sum = __int_as_float(of.y);
+    const float by0 = kCentredRows ? 1.0f : down0, by1 = kCentredRows ? 1.0f : down1;   // (what is left to be done)
+    ok = __all_sync(kAll, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns));
+    if (!ok) break;
+    tc_fence_after();
+    const uint32_t taddr = tmem + static_cast<uint32_t>(acc * kDxTile + half * (it.n / 2)) + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+    for (int c = 0; c < it.n / 128; ++c) {
+      uint8_t* place = slots + slot * kChunk;
+      uint8_t* row = place + lane * 128;
+      uint32_t v[2][32];
+      tmem_ld_32x32b_x32(taddr + c * 64, v[0]);
+      tmem_ld_32x32b_x32(taddr + c * 64 + 32, v[1]);
+      if (g.residual) {
+        ok = __all_sync(kAll, mbar_wait_bounded(&arrived[slot], (phases >> slot) & 1u, abort_flag, g.timeout_ns));
+        if (!ok) break;
+        phases ^= 1u << slot;
+      } else {
+        // the place's last store has read it
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kDxSlots - 1) : "memory");
+        __syncwarp();
+      }
+      tmem_ld_wait();
+      if (c == it.n / 128 - 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
+      }
+      if constexpr (kCentredRows) {
+        const float4* mean = reinterpret_cast<const float4*>(g.mean + it.k0 + half * (it.n / 2) + c * 64);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float4 m4 = mean[j];
+          const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t& w = v[j >> 3][4 * (j & 7) + i];
+            w = __float_as_uint(fmaf(sum, m[i], __uint_as_float(w) * down0 * down1));
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint4* at = reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4));
+        const uint4 r = g.residual ? *at : make_uint4(0, 0, 0, 0);
+        const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float2 f = unpack_bf16x2(rw[m]);
+          const int e = 8 * (j & 3) + 2 * m;
+          o[m] = pack_bf16x2(__uint_as_float(v[j >> 2][e]) * by0 * by1 + f.x, __uint_as_float(v[j >> 2][e + 1]) * by0 * by1 + f.y);
+        }
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        // (tokens past T are clipped by the map; of some there must be one)
+        if (it.t0 + row0 < g.T) tma_store_3d(&maps.out, place, it.k0 + half * (it.n / 2) + c * 64, it.t0 + row0, 0);
+        bulk_commit_group();
+        // the chunk before has been read by its store: its place is filled again
+        if (g.residual && !first) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      }
+      __syncwarp();
+      if (!first) copy_in();
+      first = false;
+      slot = slot == kDxSlots - 1 ? 0 : slot + 1;
+    }
+  }
+  if (!ok) {
+    set_status(g.status, MOE_ERR_TIMEOUT);
+    *abort_flag = 1;
+    leave_copies_time();
+  }
+  if (lane == 0) bulk_wait_all();   // this warp's stores have completed
+}
+
+// (Not inlined: beside the other form in one body it slowed that down, 2 us at 8192 x 7168 and
+// 256 experts.)
+__device__ __noinline__ void dx_epilogue_centred(uint8_t* smem, const DxMaps& maps, const DxArgs& g, int i0, uint32_t tmem) {
+  dx_epilogue<true>(smem, maps, g, i0, tmem);
 }
 
 // The work of CTA pair i0 of g.pairs.
@@ -554,103 +763,12 @@ __device__ __forceinline__ void dx_part(uint8_t* smem, const DxMaps& maps, const
     }
   } else {
     // ------------------------------------------------------------------ epilogue (both CTAs)
-    // A lane holds a token; a warp takes half of the tile's columns, 64 at a time:
-    // whole lines of memory.  The residual is copied to where the result is formed and
-    // copied out from, in three places in turn: two chunks are on their way while one is
-    // worked on.  (Loads to registers a tile ahead were waited for at the next barrier.)
-    const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* slots = smem + kDxOffSlots + (warp - 2) * kDxSlots * kChunk;   // (128-byte rows, 128-byte swizzle)
-    uint64_t* arrived = bars->arrived + (warp - 2) * kDxSlots;
-    const int row0 = static_cast<int>(rank) * 128 + quad * 32;   // of this warp in a tile
-    int next_i = i0;   // the chunk to be copied in next, and its place
-    int next_c = 0, next_slot = 0;
-    const auto copy_in = [&]() {
-      if (!g.residual || next_i >= items) return;
-      const DxItem it = dx_item(g, next_i);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&arrived[next_slot], kChunk);
-        tma_load_3d(slots + next_slot * kChunk, &maps.res, &arrived[next_slot], it.k0 + half * (it.n / 2) + next_c * 64,
-                    it.t0 + row0, 0);
-      }
-      next_slot = next_slot == kDxSlots - 1 ? 0 : next_slot + 1;
-      if (++next_c == it.n / 128) {
-        next_c = 0;
-        next_i += i_step;
-      }
-    };
-    for (int c = 0; c < kDxSlots; ++c) copy_in();
-    int slot = 0;
-    bool first = true;
-    int iter = 0;
-    bool ok = true;
-    uint32_t phases = 0;   // the places' parities
-    for (int i = i0; i < items && ok; i += i_step, ++iter) {
-      const DxItem it = dx_item(g, i);
-      const int acc = iter & 1;
-      // this lane's token: its power of two, in two factors that are numbers of their own
-      const int exp = it.t0 + row0 + lane < g.T ? g.row_exps[it.t0 + row0 + lane] : 0;
-      const float by0 = pow2(exp / 2), by1 = pow2(exp - exp / 2);
-      ok = __all_sync(kAll, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem + static_cast<uint32_t>(acc * kDxTile + half * (it.n / 2)) + (static_cast<uint32_t>(quad * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < it.n / 128; ++c) {
-        uint8_t* place = slots + slot * kChunk;
-        uint8_t* row = place + lane * 128;
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(taddr + c * 64, v[0]);
-        tmem_ld_32x32b_x32(taddr + c * 64 + 32, v[1]);
-        if (g.residual) {
-          ok = __all_sync(kAll, mbar_wait_bounded(&arrived[slot], (phases >> slot) & 1u, abort_flag, g.timeout_ns));
-          if (!ok) break;
-          phases ^= 1u << slot;
-        } else {
-          // the place's last store has read it
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kDxSlots - 1) : "memory");
-          __syncwarp();
-        }
-        tmem_ld_wait();
-        if (c == it.n / 128 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint4* at = reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4));
-          const uint4 r = g.residual ? *at : make_uint4(0, 0, 0, 0);
-          const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float2 f = unpack_bf16x2(rw[m]);
-            const int e = 8 * (j & 3) + 2 * m;
-            o[m] = pack_bf16x2(__uint_as_float(v[j >> 2][e]) * by0 * by1 + f.x, __uint_as_float(v[j >> 2][e + 1]) * by0 * by1 + f.y);
-          }
-          *at = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          // (tokens past T are clipped by the map; of some there must be one)
-          if (it.t0 + row0 < g.T) tma_store_3d(&maps.out, place, it.k0 + half * (it.n / 2) + c * 64, it.t0 + row0, 0);
-          bulk_commit_group();
-          // the chunk before has been read by its store: its place is filled again
-          if (g.residual && !first) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        }
-        __syncwarp();
-        if (!first) copy_in();
-        first = false;
-        slot = slot == kDxSlots - 1 ? 0 : slot + 1;
-      }
-    }
-    if (!ok) {
-      set_status(g.status, MOE_ERR_TIMEOUT);
-      *abort_flag = 1;
-      leave_copies_time();
-    }
-    if (lane == 0) bulk_wait_all();   // this warp's stores have completed
+    bool centred = false;   // some expert's row is less the mean
+    for (int e = lane; e < g.E; e += 32) centred |= is_centred(g.exps[e]);
+    if (__any_sync(kAll, centred))
+      dx_epilogue_centred(smem, maps, g, i0, tmem);
+    else
+      dx_epilogue<false>(smem, maps, g, i0, tmem);
   }
 }
 
@@ -988,7 +1106,7 @@ Shares shares(int64_t T, int64_t K, int32_t E) {
 
 // What the workspace holds, from its start.
 struct Places {
-  int64_t counts, tokens, exps, parts, row_exps, planes, half, w_half, sums, total;
+  int64_t counts, tokens, exps, parts, mean, rows, planes, half, w_half, sums, total;
   Shares shares;
 };
 Places places(int64_t T, int64_t K, int32_t E) {
@@ -997,8 +1115,9 @@ Places places(int64_t T, int64_t K, int32_t E) {
   p.counts = 64;
   p.exps = p.counts + 4 * static_cast<int64_t>(E);
   p.parts = up(p.exps + 4 * static_cast<int64_t>(E), 256);
-  p.row_exps = p.parts + 8 * cuts(T, kDzWarps);
-  p.planes = up(p.row_exps + 4 * T, 256);
+  p.mean = up(p.parts + 8 * cuts(T, kDzWarps), 256);
+  p.rows = up(p.mean + 4 * K, 256);
+  p.planes = up(p.rows + 8 * T, 256);
   p.half = up(p.planes + T * 3 * up(E, 64) * 2, 256);
   p.w_half = up(p.half + T * up(E, 64) * 2, 256);
   p.sums = up(p.w_half + static_cast<int64_t>(E) * K * 2, 256);
@@ -1091,7 +1210,8 @@ moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, c
   uint16_t* half = reinterpret_cast<uint16_t*>(base + at.half);
   uint16_t* w_half = reinterpret_cast<uint16_t*>(base + at.w_half);
   int32_t* exps = reinterpret_cast<int32_t*>(base + at.exps);
-  int32_t* row_exps = reinterpret_cast<int32_t*>(base + at.row_exps);
+  float* mean = reinterpret_cast<float*>(base + at.mean);
+  int2* rows = reinterpret_cast<int2*>(base + at.rows);
   if ((st = box_map(&dx_maps.dz, half, T, Ep, 128, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != MOE_OK) return st;
   if ((st = box_map(&dx_maps.w, w_half, E, K, kDxBlock, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != MOE_OK) return st;
   if ((st = box_map(&dx_maps.out, dx_bf16, T, K, 32)) != MOE_OK) return st;
@@ -1099,12 +1219,14 @@ moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, c
 
   int32_t* counts = reinterpret_cast<int32_t*>(base + at.counts);
   int32_t* tokens = reinterpret_cast<int32_t*>(base + at.tokens);
-  const PrepareArgs prepare = {topk_ids, kept, T, topk, E, counts, tokens, status, static_cast<const uint4*>(w_planes), K / 8,
+  const uint4* w = static_cast<const uint4*>(w_planes);
+  const PrepareArgs prepare = {topk_ids, kept, T, topk, E, counts, tokens, status, w, K / 8, mean,
                                reinterpret_cast<uint4*>(w_half), exps};
   MOE_TRY(launch_pdl_cluster(route_prepare_kernel, dim3(static_cast<unsigned>(kCountCtas + up(E, kCountCtas))),
                              dim3(kPrepareThreads), 0, s, kCountCtas, prepare));
   DzArgs z = {logits, topk_ids, topk_weights, dweights, kept, T, E, Ep, topk, static_cast<float>(balance),
-              static_cast<float>(zloss), counts, tokens, exps, planes, half, row_exps, dlogits, reinterpret_cast<float2*>(base + at.parts)};
+              static_cast<float>(zloss), counts, tokens, exps, planes, half, rows, dlogits,
+              reinterpret_cast<float2*>(base + at.parts)};
   MOE_TRY((E <= 64 ? launch_dz<1> : E <= 128 ? launch_dz<2> : E <= 256 ? launch_dz<4> : E <= 512 ? launch_dz<8>
                                                                                             : launch_dz<16>)(z, s));
   DxArgs d;
@@ -1115,7 +1237,10 @@ moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, c
   d.k_tiles = static_cast<int32_t>(cuts(K, kDxTile));
   d.T = T;
   d.K = K;
-  d.row_exps = row_exps;
+  d.rows = rows;
+  d.exps = exps;
+  d.mean = mean;
+  d.E = E;
   d.residual = residual != nullptr;
   d.status = status;
   d.timeout_ns = 2000000000ull;
