@@ -620,8 +620,10 @@ __global__ void __launch_bounds__(Cfg<kOp>::kThreads, 1)
         }
         if (left <= 0) continue;   // warp-uniform
         if constexpr (kFwdOne || kOp == kFwdGlu) {
+          if (g.bias) {   // (-0 + 0 is 0: without one nothing is added)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + bias);
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + bias);
+          }
         }
         if constexpr (kFwdOne || kZ || kRes) {
           float2 p[16];

@@ -319,8 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint16_t* out = g.out + at_row * g.out_ld + col;
             if constexpr (kWay == kFewFwdGlu) {
               float2 p = *reinterpret_cast<const float2*>(tile + row * 64 + 32 + 2 * pair);
-              s = make_float2(s.x + b.x, s.y + b.y);
-              p = make_float2(p.x + bu.x, p.y + bu.y);
+              if (g.bias) {   // (nothing is added where there is nothing: -0 + 0 is 0)
+                s = make_float2(s.x + b.x, s.y + b.y);
+                p = make_float2(p.x + bu.x, p.y + bu.y);
+              }
               if (g.keep) {
                 uint16_t* keep = g.keep + at_row * g.keep_ld + col;
                 *reinterpret_cast<uint32_t*>(keep) = pack_bf16x2(s.x, s.y);
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint32_t*>(out + g.cols) = pack_bf16x2(s.x * value.x, s.y * value.y);
             } else {
               if constexpr (kWay == kFewFwd) {
-                s = make_float2(s.x + b.x, s.y + b.y);
+                if (g.bias) s = make_float2(s.x + b.x, s.y + b.y);
                 if (g.keep) *reinterpret_cast<uint32_t*>(g.keep + at_row * g.keep_ld + col) = pack_bf16x2(s.x, s.y);
                 s = make_float2(act_at<kA, false>(s.x, nullptr), act_at<kA, false>(s.y, nullptr));
               } else if constexpr (kA != MOE_ACT_NONE) {
@@ -347,8 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 act_at<kA, true>(at.y, &slope.y);
                 s = make_float2(__fmul_rn(s.x, slope.x), __fmul_rn(s.y, slope.y));
               }
-              const float2 a = unpack_bf16x2(r[i]);
-              *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y));
+              if (g.res) {
+                const float2 a = unpack_bf16x2(r[i]);
+                s = make_float2(__fadd_rn(s.x, a.x), __fadd_rn(s.y, a.y));
+              }
+              *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(s.x, s.y);
             }
           }
         });
