@@ -14,7 +14,7 @@
 // P: the rational approximation 7.1.26 of Abramowitz and Stegun's handbook,
 // erfc(a) = t (a1 + t (a2 + ...)) exp(-a^2) with t = 1 / (1 + p a), whose error is
 // at most 1.5e-7; the tail below 0 is taken as it is, not as 1 minus the rest.
-// NaN stays NaN in all of them.  A product is rounded before something is added to it
+// NaN stays NaN in all of them, values and derivatives.  A product is rounded before something is added to it
 // (__fmul_rn, __fadd_rn where a compiler might join them), so that kernels of different
 // shapes give the same bits.
 #pragma once
@@ -56,6 +56,13 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // 1 / (1 + exp(-x)); 0 below x = -87.3, where it is less than 2^-126.
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + ex2_fast(x * -1.44269504f)); }
 
+// max(z, 0), NaN for NaN (z <= 0 ? 0 : z in one instruction).
+__device__ __forceinline__ float not_below_0(float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+  return r;
+}
+
 // The activation's value and, where it is asked for, its slope at z.
 template <int kAct, bool kSlope>
 __device__ __forceinline__ float act_at(float z, float* slope) {
@@ -81,10 +88,11 @@ __device__ __forceinline__ float act_at(float z, float* slope) {
     if constexpr (kSlope) *slope = fmaf(v * (1.0f - s), fmaf(zz, 0.21406444f, 1.59576912f), s);
     return v;
   } else if constexpr (kAct == MOE_ACT_RELU) {
-    if constexpr (kSlope) *slope = z > 0.0f ? 1.0f : 0.0f;
-    return z <= 0.0f ? 0.0f : z;
+    const float r = not_below_0(z);
+    if constexpr (kSlope) *slope = r > 0.0f ? 1.0f : r;
+    return r;
   } else if constexpr (kAct == MOE_ACT_RELU2) {
-    const float r = z <= 0.0f ? 0.0f : z;
+    const float r = not_below_0(z);
     if constexpr (kSlope) *slope = 2.0f * r;
     return r * r;
   } else {
