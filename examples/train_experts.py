@@ -148,10 +148,10 @@ class Router:
         self.ids, self.weights, self.logits = M.moe_route(x, self.planes, self.topk)
         return self.ids, self.weights
 
-    def backward(self, x, dweights, dx, accumulate=False):
-        """Gradient of w; dx += that of x."""
-        M.moe_route_backward(x, self.planes, self.logits, self.ids, self.weights, dweights, balance=self.balance,
-                             zloss=self.zloss, residual=dx, dx=dx, dw=self.dw, accumulate=accumulate, losses=self.losses,
+    def backward(self, x, dweights, dx, accumulate=False, batches=1):
+        """Gradient of w; dx += that of x.  Of a mean over batches: the losses count 1 / batches, as dweights do."""
+        M.moe_route_backward(x, self.planes, self.logits, self.ids, self.weights, dweights, balance=self.balance / batches,
+                             zloss=self.zloss / batches, residual=dx, dx=dx, dw=self.dw, accumulate=accumulate, losses=self.losses,
                              ws=self.ws)
         torch.maximum(self.status[:1], self.ws[:4].view(torch.int32), out=self.status[:1])
         return self.dw
@@ -216,7 +216,7 @@ def train(T=512, K=256, I=256, E=8, topk=2, steps=30, state_bits=8, lr=3e-3, cli
             if shared:
                 more.backward(dout, x, layer.dx)
             if train_router:
-                router.backward(x, layer.dweights, layer.dx, accumulate=part > 0)
+                router.backward(x, layer.dweights, layer.dx, accumulate=part > 0, batches=batches_per_step)
         losses.append(loss)
         norm = torch.stack([g.float().norm() for g in (layer.dw13, layer.dw2, *(g for _, g in others))]).norm()
         scale = (clip / norm).clamp(max=1.0).reshape(1)   # stays on the device
