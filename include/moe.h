@@ -442,7 +442,8 @@ moe_status_t moe_expert_gemm_wgrad(const void* dy, int64_t dy_ld, const void* x,
  *                              expert without rows; accumulate != 0: added to db
  *                              db fp32 [E, N]; N a multiple of 8
  * A residual may be the output itself (added to in place); no other output may
- * overlap an input.  The exponential and the reciprocal are good to 2^-21, and
+ * overlap an input.  exp(v) is good to (4 + 3 |v|) 2^-23 of itself (its argument is
+ * rounded to fp32 before the base-2 exponential), the reciprocal to 2^-22, and
  * MOE_ACT_GELU's erf to 1.5e-7. */
 moe_status_t moe_expert_gemm_act(const void* x, int64_t x_ld, int64_t rows, const void* w, const void* bias,
                                  int32_t bias_elem, int32_t act, const void* residual, int64_t residual_ld,

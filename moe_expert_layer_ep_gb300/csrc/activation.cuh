@@ -2,7 +2,8 @@
 // in fp32, for the epilogues: by the hardware's base-2 exponential and
 // reciprocal, both within 2 ulp, because an epilogue is bound by the
 // instructions it issues (an IEEE quotient costs as much as the rest) and its
-// results are rounded to bf16.
+// results are rounded to bf16.  The exponential's argument v log2(e) is rounded
+// first, which is what is left of exp(v) far from 0: (4 + 3 |v|) 2^-23 of it.
 //
 //   silu       z s,  s = 1 / (1 + exp(-z));          s (1 + z (1 - s))
 //   gelu       z P,  P = (1 + erf(z / sqrt 2)) / 2;  P + z exp(-z^2 / 2) / sqrt(2 pi)
