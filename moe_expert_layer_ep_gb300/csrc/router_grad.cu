@@ -72,9 +72,10 @@ constexpr int kMeanOf = 4;       // experts, evenly spread, whose mean row is ta
 // than this share of what it was: rows that have nothing in common, whose mean is an accident
 // of the drawing, stay as they are, and so does an expert beside another of much larger
 // weights, whose mean would only be put into its row.  (Any row near the mean of all would
-// do, since what is taken off is put back: the mean of four leaves rows 1.12 times as large
-// as that of all, and each CTA forms it for itself, while the assignments are counted: of
-// eight, 1.06 times, 2.7 us more at 256 experts of 7168; of all, by a kernel before, 4 to 7.)
+// do, since what is taken off is put back: hence its rounding to bf16.  The mean of four
+// leaves rows 1.12 times as large as that of all, and each CTA forms it for itself, while
+// the assignments are counted: of eight, 1.06 times, 2.7 us more at 256 experts of 7168; of
+// all, by a kernel before, 4 to 7.)
 constexpr float kCentred = 0.7f;
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }   // |e| <= 126
@@ -118,7 +119,7 @@ struct PrepareArgs {
   int32_t* status;
   const uint4* planes;     // W [3][E][K]
   int64_t row8;            // K / 8
-  float* mean;             // [K]
+  uint4* mean;             // [K] in bf16
   uint4* half;             // [E][K]
   int32_t* exps;           // [E] the power of two, and 2^16 where the row is less the mean
 };
@@ -136,7 +137,7 @@ __device__ __forceinline__ void half_row(const PrepareArgs& g, int e) {
   const uint4* lo = mid + g.E * g.row8;
   const auto load = [&](const uint4* plane, int64_t i, float (&v)[8]) { unpack8(plane[i], v); };
   const int of = min(kMeanOf, g.E);
-  const auto load_mean = [&](int64_t i, float (&v)[8]) {   // of the first planes
+  const auto load_mean = [&](int64_t i, float (&v)[8]) {   // of the first planes; also its words in bf16
     uint4 w[kMeanOf];
 #pragma unroll
     for (int n = 0; n < kMeanOf; ++n) w[n] = n < of ? g.planes[n * g.E / of * g.row8 + i] : make_uint4(0, 0, 0, 0);
@@ -150,20 +151,18 @@ __device__ __forceinline__ void half_row(const PrepareArgs& g, int e) {
       for (int j = 0; j < 8; ++j) v[j] += a[j];
     }
     const float share = 1.0f / static_cast<float>(of);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= share;
+    const uint4 words = make_uint4(pack_bf16x2(v[0] * share, v[1] * share), pack_bf16x2(v[2] * share, v[3] * share),
+                                   pack_bf16x2(v[4] * share, v[5] * share), pack_bf16x2(v[6] * share, v[7] * share));
+    unpack8(words, v);
+    return words;
   };
   float4 seen = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // largest and sum, as it is; largest and sum, without the mean
   for (int64_t i = threadIdx.x; i < g.row8; i += kPrepareThreads) {
     float a[8], b[8], m[8];
     load(hi, i, a);
     load(mid, i, b);
-    load_mean(i, m);
-    if (e == 0) {
-      float4* mean = reinterpret_cast<float4*>(g.mean) + 2 * i;
-      mean[0] = make_float4(m[0], m[1], m[2], m[3]);
-      mean[1] = make_float4(m[4], m[5], m[6], m[7]);
-    }
+    const uint4 words = load_mean(i, m);
+    if (e == 0) g.mean[i] = words;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float w = a[j] + b[j], c = fabsf(w - m[j]);
@@ -485,7 +484,7 @@ struct DxArgs {
   int64_t T, K;
   const int2* rows;        // [T] (DzArgs)
   const int32_t* exps;     // [E] (PrepareArgs)
-  const float* mean;       // [K]
+  const uint4* mean;       // [K] in bf16 (PrepareArgs)
   int32_t E;
   int32_t residual;
   int32_t* status;
@@ -587,8 +586,7 @@ __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, c
     // this lane's token: its power of two, in two factors that are numbers of their own
     const int2 of = it.t0 + row0 + lane < g.T ? g.rows[it.t0 + row0 + lane] : make_int2(0, 0);
     const int exp = of.x;
-    const float down0 = pow2(exp / 2), down1 = pow2(exp - exp / 2), sum = __int_as_float(of.y);
-    const float by0 = kCentredRows ? 1.0f : down0, by1 = kCentredRows ? 1.0f : down1;   // (what is left to be done)
+    const float by0 = pow2(exp / 2), by1 = pow2(exp - exp / 2), sum = __int_as_float(of.y);
     ok = __all_sync(kAll, mbar_wait_bounded(&tfull[acc], (iter >> 1) & 1, abort_flag, g.timeout_ns));
     if (!ok) break;
     tc_fence_after();
@@ -600,6 +598,11 @@ __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, c
       uint32_t v[2][32];
       tmem_ld_32x32b_x32(taddr + c * 64, v[0]);
       tmem_ld_32x32b_x32(taddr + c * 64 + 32, v[1]);
+      uint4 mean[kCentredRows ? 8 : 1];   // of the 64 columns, the same in every lane
+      if constexpr (kCentredRows) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mean[j] = g.mean[(it.k0 + half * (it.n / 2) + c * 64) / 8 + j];
+      }
       if (g.residual) {
         ok = __all_sync(kAll, mbar_wait_bounded(&arrived[slot], (phases >> slot) & 1u, abort_flag, g.timeout_ns));
         if (!ok) break;
@@ -615,30 +618,24 @@ __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, c
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&tempty[acc]), 0));
       }
-      if constexpr (kCentredRows) {
-        const float4* mean = reinterpret_cast<const float4*>(g.mean + it.k0 + half * (it.n / 2) + c * 64);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float4 m4 = mean[j];
-          const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t& w = v[j >> 3][4 * (j & 7) + i];
-            w = __float_as_uint(fmaf(sum, m[i], __uint_as_float(w) * down0 * down1));
-          }
-        }
-      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint4* at = reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4));
         const uint4 r = g.residual ? *at : make_uint4(0, 0, 0, 0);
         const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
         uint32_t o[4];
+        float common[8];
+        if constexpr (kCentredRows) unpack8(mean[j], common);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const float2 f = unpack_bf16x2(rw[m]);
           const int e = 8 * (j & 3) + 2 * m;
-          o[m] = pack_bf16x2(__uint_as_float(v[j >> 2][e]) * by0 * by1 + f.x, __uint_as_float(v[j >> 2][e + 1]) * by0 * by1 + f.y);
+          float a = __uint_as_float(v[j >> 2][e]) * by0 * by1, b = __uint_as_float(v[j >> 2][e + 1]) * by0 * by1;
+          if constexpr (kCentredRows) {
+            a = fmaf(sum, common[2 * m], a);
+            b = fmaf(sum, common[2 * m + 1], b);
+          }
+          o[m] = pack_bf16x2(a + f.x, b + f.y);
         }
         *at = make_uint4(o[0], o[1], o[2], o[3]);
       }
@@ -666,9 +663,11 @@ __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, c
 }
 
 // (Not inlined: beside the other form in one body it slowed that down, 2 us at 8192 x 7168 and
-// 256 experts.)
+// 256 experts.  There a call takes 128 us with a common row, 107 without: the mean passes
+// through shared memory's path to the registers too, 512 of a tile's cycles in bf16.)
 __device__ __noinline__ void dx_epilogue_centred(uint8_t* smem, const DxMaps& maps, const DxArgs& g, int i0, uint32_t tmem) {
-  dx_epilogue<true>(smem, maps, g, i0, tmem);
+  const DxArgs mine = g;   // (in registers: read again after every barrier they cost 20 us more)
+  dx_epilogue<true>(smem, maps, mine, i0, tmem);
 }
 
 // The work of CTA pair i0 of g.pairs.
@@ -1116,7 +1115,7 @@ Places places(int64_t T, int64_t K, int32_t E) {
   p.exps = p.counts + 4 * static_cast<int64_t>(E);
   p.parts = up(p.exps + 4 * static_cast<int64_t>(E), 256);
   p.mean = up(p.parts + 8 * cuts(T, kDzWarps), 256);
-  p.rows = up(p.mean + 4 * K, 256);
+  p.rows = up(p.mean + 2 * K, 256);
   p.planes = up(p.rows + 8 * T, 256);
   p.half = up(p.planes + T * 3 * up(E, 64) * 2, 256);
   p.w_half = up(p.half + T * up(E, 64) * 2, 256);
@@ -1210,7 +1209,7 @@ moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, c
   uint16_t* half = reinterpret_cast<uint16_t*>(base + at.half);
   uint16_t* w_half = reinterpret_cast<uint16_t*>(base + at.w_half);
   int32_t* exps = reinterpret_cast<int32_t*>(base + at.exps);
-  float* mean = reinterpret_cast<float*>(base + at.mean);
+  uint4* mean = reinterpret_cast<uint4*>(base + at.mean);
   int2* rows = reinterpret_cast<int2*>(base + at.rows);
   if ((st = box_map(&dx_maps.dz, half, T, Ep, 128, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != MOE_OK) return st;
   if ((st = box_map(&dx_maps.w, w_half, E, K, kDxBlock, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != MOE_OK) return st;
