@@ -4,8 +4,8 @@
 // whole reduction and at most 64 rows (its N, 8 to 64): 2048 features are 32 CTAs, where
 // tiles of 256 features on CTA pairs are 16, and there is no pair to set up.  The sum of an
 // output runs over the reduction in the same steps of the tensor cores as there, so a
-// row's bits are those of the larger batches; splitting the reduction over CTAs would
-// change them.
+// row's bits are those of the larger batches; splitting the reduction over CTAs here alone
+// would change them (segments of one length in every dense kernel would not).
 //
 // What bounds it.  One row of 7168 by 2048 features takes 14 us (those tiles 26.5; the
 // weights' bytes 4.3), by 7168 features 18.3 (28.9; 15.1), 2048 by 7168 7.7 (12.5; 4.3).  A
