@@ -489,10 +489,10 @@ moe_status_t moe_expert_bias_grad(const void* dy, int64_t dy_ld, int64_t rows, c
  *   dw fp32 [E_global, K] = dz^T x; accumulate != 0: added to dw
  * dlogits (dz, fp32 [T, E_global]) and losses (fp32 [2]) may be NULL.  dz and dW's
  * products in fp32 (dW's sums over 256 tokens at a time, then in order); for dx, dz
- * and W are taken with 11 significant bits, and summed in fp32: W's rows less the mean
- * row of up to four experts (e E_global / 4) where that leaves less than 0.7 of a row's
- * sum of sizes, and dz's sum over those rows times the mean row in fp32, since what
- * rows have in common cancels in a dz that sums to 0.  The same bits every
+ * and W are taken with 11 significant bits, and summed in fp32: W's rows less
+ * another where that leaves less than 0.7 of a row's sum of sizes, and dz's sum over
+ * those rows times that one in fp32, since what rows have in common cancels in a dz
+ * that sums to 0 (per column, the middle of four experts' values, in bf16).  The same bits every
  * time.  Limits as for moe_route, K <= 2^30 and fewer than 2^31
  * assignments; logits may be -infinity, not
  * all of a token's.  ws: device scratch, 16-byte aligned, at least

@@ -11,9 +11,9 @@
 //   dx      = dz W + residual (bf16),   dW = dz^T x (fp32)
 //
 // Three kernels, and a fourth where dW's sums were split:
-//   route_prepare_kernel assignments per expert and tokens that have one; W in fp16, less the
-//                        mean row m of four experts where that makes an expert's row clearly
-//                        smaller, each expert's row times a power of two
+//   route_prepare_kernel assignments per expert and tokens that have one; W in fp16, less a
+//                        row m that they have in common where that makes an expert's row
+//                        clearly smaller, each expert's row times a power of two
 //   route_dz_kernel      a warp per token: dz in three bf16 planes whose sum it is (as
 //                        moe_router_prepare splits the weights) and, for dx, in fp16
 //                        times a power of two, without the weights' own; its sum over the
@@ -67,15 +67,14 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 // ---------------------------------------------------------------------------
 constexpr int kPrepareThreads = 512;
 constexpr int kCountCtas = 8;
-constexpr int kMeanOf = 4;       // experts, evenly spread, whose mean row is taken
-// An expert's row is taken less the mean row where the sum of its sizes becomes smaller
-// than this share of what it was: rows that have nothing in common, whose mean is an accident
-// of the drawing, stay as they are, and so does an expert beside another of much larger
-// weights, whose mean would only be put into its row.  (Any row near the mean of all would
-// do, since what is taken off is put back: hence its rounding to bf16.  The mean of four
-// leaves rows 1.12 times as large as that of all, and each CTA forms it for itself, while
-// the assignments are counted: of eight, 1.06 times, 2.7 us more at 256 experts of 7168; of
-// all, by a kernel before, 4 to 7.)
+// m, per column: the middle of the values of four evenly spread experts (of the second and
+// third in order), rounded to bf16.  Any row near what rows have in common would do, since
+// what is taken off is put back; the middle is not moved by an expert, or a value, unlike the
+// others, and each CTA forms it for itself, while the assignments are counted.  (The mean of
+// eight took 2.7 us more at 256 experts of 7168, of all, by a kernel before, 4 to 7.)
+// An expert's row is taken less m where the sum of its sizes becomes smaller than this share
+// of what it was: rows that have nothing in common, whose middle is an accident of the
+// drawing, stay as they are.
 constexpr float kCentred = 0.7f;
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }   // |e| <= 126
@@ -119,16 +118,16 @@ struct PrepareArgs {
   int32_t* status;
   const uint4* planes;     // W [3][E][K]
   int64_t row8;            // K / 8
-  uint4* mean;             // [K] in bf16
+  uint4* common;           // [K] m in bf16
   uint4* half;             // [E][K]
-  int32_t* exps;           // [E] the power of two, and 2^16 where the row is less the mean
+  int32_t* exps;           // [E] the power of two, and 2^16 where the row is less m
 };
 
 // What exps holds.
 __device__ __forceinline__ int exp_of(int32_t w) { return static_cast<int16_t>(w); }
 __device__ __forceinline__ bool is_centred(int32_t w) { return (w >> 16 & 1) != 0; }
 
-// Row e of W, or what is left of it without the mean row, times 2^exp in fp16, its largest
+// Row e of W, or what is left of it without m, times 2^exp in fp16, its largest
 // value in [2^14, 2^15) (exp within +-126).
 __device__ __forceinline__ void half_row(const PrepareArgs& g, int e) {
   __shared__ float4 s_part[kPrepareThreads / 32];
@@ -136,33 +135,27 @@ __device__ __forceinline__ void half_row(const PrepareArgs& g, int e) {
   const uint4* mid = hi + g.E * g.row8;
   const uint4* lo = mid + g.E * g.row8;
   const auto load = [&](const uint4* plane, int64_t i, float (&v)[8]) { unpack8(plane[i], v); };
-  const int of = min(kMeanOf, g.E);
-  const auto load_mean = [&](int64_t i, float (&v)[8]) {   // of the first planes; also its words in bf16
-    uint4 w[kMeanOf];
+  const auto load_middle = [&](int64_t i, float (&v)[8]) {   // of the first planes; also its words in bf16
+    float w[4][8];
 #pragma unroll
-    for (int n = 0; n < kMeanOf; ++n) w[n] = n < of ? g.planes[n * g.E / of * g.row8 + i] : make_uint4(0, 0, 0, 0);
+    for (int n = 0; n < 4; ++n) load(g.planes + n * g.E / 4 * g.row8, i, w[n]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < kMeanOf; ++n) {
-      float a[8];
-      unpack8(w[n], a);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += a[j];
+    for (int j = 0; j < 8; ++j) {
+      const float lower = fmaxf(fminf(w[0][j], w[1][j]), fminf(w[2][j], w[3][j]));
+      const float upper = fminf(fmaxf(w[0][j], w[1][j]), fmaxf(w[2][j], w[3][j]));
+      v[j] = 0.5f * lower + 0.5f * upper;
     }
-    const float share = 1.0f / static_cast<float>(of);
-    const uint4 words = make_uint4(pack_bf16x2(v[0] * share, v[1] * share), pack_bf16x2(v[2] * share, v[3] * share),
-                                   pack_bf16x2(v[4] * share, v[5] * share), pack_bf16x2(v[6] * share, v[7] * share));
+    const uint4 words = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     unpack8(words, v);
     return words;
   };
-  float4 seen = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // largest and sum, as it is; largest and sum, without the mean
+  float4 seen = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // largest and sum, as it is; largest and sum, without m
   for (int64_t i = threadIdx.x; i < g.row8; i += kPrepareThreads) {
     float a[8], b[8], m[8];
     load(hi, i, a);
     load(mid, i, b);
-    const uint4 words = load_mean(i, m);
-    if (e == 0) g.mean[i] = words;
+    const uint4 words = load_middle(i, m);
+    if (e == 0) g.common[i] = words;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float w = a[j] + b[j], c = fabsf(w - m[j]);
@@ -195,7 +188,7 @@ __device__ __forceinline__ void half_row(const PrepareArgs& g, int e) {
     if (centred) {   // (the last plane too: it is 2^-17 of what was common)
       float m[8];
       load(lo, i, b);
-      load_mean(i, m);
+      load_middle(i, m);
 #pragma unroll
       for (int j = 0; j < 8; ++j) a[j] = a[j] + b[j] - m[j];
     }
@@ -285,7 +278,7 @@ struct DzArgs {
   uint16_t* planes;        // [T][3][Ep]
   uint16_t* half;          // [T][Ep] dz 2^-exps, times a power of two of the row, in fp16
   int2* rows;              // [T] 2 to the first's power: what the row's product is multiplied by;
-                           // the second, a float: dz's sum over the experts whose rows are less the mean
+                           // the second, a float: dz's sum over the experts whose rows are less m
   float* dlogits;          // [T, E] or null
   float2* parts;           // [gridDim.x] sums of a CTA's tokens
 };
@@ -484,7 +477,7 @@ struct DxArgs {
   int64_t T, K;
   const int2* rows;        // [T] (DzArgs)
   const int32_t* exps;     // [E] (PrepareArgs)
-  const uint4* mean;       // [K] in bf16 (PrepareArgs)
+  const uint4* common;     // [K] m in bf16 (PrepareArgs)
   int32_t E;
   int32_t residual;
   int32_t* status;
@@ -541,7 +534,7 @@ __device__ __forceinline__ void dx_init(uint8_t* smem, const DxMaps& maps) {
   prefetch_tensormap(&maps.out);
 }
 
-// kCentredRows: some expert's row is less the mean, and dz's sums times the mean are added.
+// kCentredRows: some expert's row is less m, and dz's sums times m are added.
 template <bool kCentredRows>
 __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, const DxArgs& g, int i0, uint32_t tmem) {
   DxBars* bars = reinterpret_cast<DxBars*>(smem + kDxOffBars);
@@ -598,10 +591,10 @@ __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, c
       uint32_t v[2][32];
       tmem_ld_32x32b_x32(taddr + c * 64, v[0]);
       tmem_ld_32x32b_x32(taddr + c * 64 + 32, v[1]);
-      uint4 mean[kCentredRows ? 8 : 1];   // of the 64 columns, the same in every lane
+      uint4 m_words[kCentredRows ? 8 : 1];   // of the 64 columns, the same in every lane
       if constexpr (kCentredRows) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mean[j] = g.mean[(it.k0 + half * (it.n / 2) + c * 64) / 8 + j];
+        for (int j = 0; j < 8; ++j) m_words[j] = g.common[(it.k0 + half * (it.n / 2) + c * 64) / 8 + j];
       }
       if (g.residual) {
         ok = __all_sync(kAll, mbar_wait_bounded(&arrived[slot], (phases >> slot) & 1u, abort_flag, g.timeout_ns));
@@ -625,7 +618,7 @@ __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, c
         const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
         uint32_t o[4];
         float common[8];
-        if constexpr (kCentredRows) unpack8(mean[j], common);
+        if constexpr (kCentredRows) unpack8(m_words[j], common);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const float2 f = unpack_bf16x2(rw[m]);
@@ -663,7 +656,7 @@ __device__ __forceinline__ void dx_epilogue(uint8_t* smem, const DxMaps& maps, c
 }
 
 // (Not inlined: beside the other form in one body it slowed that down, 2 us at 8192 x 7168 and
-// 256 experts.  There a call takes 128 us with a common row, 107 without: the mean passes
+// 256 experts.  There a call takes 128 us with a common row, 107 without: m passes
 // through shared memory's path to the registers too, 512 of a tile's cycles in bf16.)
 __device__ __noinline__ void dx_epilogue_centred(uint8_t* smem, const DxMaps& maps, const DxArgs& g, int i0, uint32_t tmem) {
   const DxArgs mine = g;   // (in registers: read again after every barrier they cost 20 us more)
@@ -762,7 +755,7 @@ __device__ __forceinline__ void dx_part(uint8_t* smem, const DxMaps& maps, const
     }
   } else {
     // ------------------------------------------------------------------ epilogue (both CTAs)
-    bool centred = false;   // some expert's row is less the mean
+    bool centred = false;   // some expert's row is less m
     for (int e = lane; e < g.E; e += 32) centred |= is_centred(g.exps[e]);
     if (__any_sync(kAll, centred))
       dx_epilogue_centred(smem, maps, g, i0, tmem);
@@ -1105,7 +1098,7 @@ Shares shares(int64_t T, int64_t K, int32_t E) {
 
 // What the workspace holds, from its start.
 struct Places {
-  int64_t counts, tokens, exps, parts, mean, rows, planes, half, w_half, sums, total;
+  int64_t counts, tokens, exps, parts, common, rows, planes, half, w_half, sums, total;
   Shares shares;
 };
 Places places(int64_t T, int64_t K, int32_t E) {
@@ -1114,8 +1107,8 @@ Places places(int64_t T, int64_t K, int32_t E) {
   p.counts = 64;
   p.exps = p.counts + 4 * static_cast<int64_t>(E);
   p.parts = up(p.exps + 4 * static_cast<int64_t>(E), 256);
-  p.mean = up(p.parts + 8 * cuts(T, kDzWarps), 256);
-  p.rows = up(p.mean + 2 * K, 256);
+  p.common = up(p.parts + 8 * cuts(T, kDzWarps), 256);
+  p.rows = up(p.common + 2 * K, 256);
   p.planes = up(p.rows + 8 * T, 256);
   p.half = up(p.planes + T * 3 * up(E, 64) * 2, 256);
   p.w_half = up(p.half + T * up(E, 64) * 2, 256);
@@ -1209,7 +1202,7 @@ moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, c
   uint16_t* half = reinterpret_cast<uint16_t*>(base + at.half);
   uint16_t* w_half = reinterpret_cast<uint16_t*>(base + at.w_half);
   int32_t* exps = reinterpret_cast<int32_t*>(base + at.exps);
-  uint4* mean = reinterpret_cast<uint4*>(base + at.mean);
+  uint4* common = reinterpret_cast<uint4*>(base + at.common);
   int2* rows = reinterpret_cast<int2*>(base + at.rows);
   if ((st = box_map(&dx_maps.dz, half, T, Ep, 128, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != MOE_OK) return st;
   if ((st = box_map(&dx_maps.w, w_half, E, K, kDxBlock, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != MOE_OK) return st;
@@ -1219,7 +1212,7 @@ moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, c
   int32_t* counts = reinterpret_cast<int32_t*>(base + at.counts);
   int32_t* tokens = reinterpret_cast<int32_t*>(base + at.tokens);
   const uint4* w = static_cast<const uint4*>(w_planes);
-  const PrepareArgs prepare = {topk_ids, kept, T, topk, E, counts, tokens, status, w, K / 8, mean,
+  const PrepareArgs prepare = {topk_ids, kept, T, topk, E, counts, tokens, status, w, K / 8, common,
                                reinterpret_cast<uint4*>(w_half), exps};
   MOE_TRY(launch_pdl_cluster(route_prepare_kernel, dim3(static_cast<unsigned>(kCountCtas + up(E, kCountCtas))),
                              dim3(kPrepareThreads), 0, s, kCountCtas, prepare));
@@ -1238,7 +1231,7 @@ moe_status_t moe_route_backward_kept(const void* x_bf16, const void* w_planes, c
   d.K = K;
   d.rows = rows;
   d.exps = exps;
-  d.mean = mean;
+  d.common = common;
   d.E = E;
   d.residual = residual != nullptr;
   d.status = status;

@@ -1,7 +1,7 @@
 """dx of the router's gradient where the rows of W have something in common, which cancels in a dz that sums to 0.
 
-W_e = W'_e + a_e m, with m the mean row of four evenly spread experts (of their first bf16 plane, summed in fp32, rounded
-to bf16) and a_e = 1 where that makes the sum of a row's sizes less than 0.7 of what it is; then dx = dz W' + (sum over a_e = 1 of dz_e) m.  Tolerance, U = 2^-23,
+W_e = W'_e + a_e m, with m, per column, the middle of four evenly spread experts' values (of their first bf16 plane: half
+the second and third in order, rounded to bf16) and a_e = 1 where that makes the sum of a row's sizes less than 0.7 of what it is; then dx = dz W' + (sum over a_e = 1 of dz_e) m.  Tolerance, U = 2^-23,
 an fp32 operation 2^-24: W' and dz are taken with 11 bits (2^-10 of sum |dz W'| for both, 1.01 for their product and,
 where a_e = 0, the plane of W that is left out, 2^-17 of W), the sum over the experts with (E / 16 + 16) U; W' is rounded
 to fp32 from W and m (U (|W| + |m|)); the sum of dz is off by (E / 32 + 8) U of its sizes, its product with m and their addition by U; what dz itself is off, as in test_gpu_route_backward.py; 2^-37 E
@@ -24,11 +24,8 @@ def _check(c, balance, zloss, residual=False):
     dz, near, _, _ = c.reference(balance, zloss)
     dx = _f64(c.run(balance, zloss, residual=c.res.cuda() if residual else None)[0])
     w, E = _f64(c.w), c.E
-    of = c.w.to(torch.bfloat16).float()[[n * E // min(4, E) for n in range(min(4, E))]]
-    mean = torch.zeros(c.K)
-    for row in of:
-        mean = mean + row
-    m = _f64((mean * (torch.ones(1) / len(of))).to(torch.bfloat16))
+    four = c.w.to(torch.bfloat16).float()[[n * E // 4 for n in range(4)]].sort(dim=0).values
+    m = _f64((0.5 * four[1] + 0.5 * four[2]).to(torch.bfloat16))
     am = np.abs(m)
     was, left = np.abs(w).sum(1), np.abs(w - m).sum(1)
     assert not np.any(np.abs(left - 0.7 * was) < 1e-4 * was)   # no row at the rule's edge
@@ -72,13 +69,20 @@ def test_common_to_some_experts():
 
 
 def test_beside_an_expert_of_large_weights():
-    """Its row fills the mean, which is then taken off no other."""
+    """Beside one, or one that has a few large values, the others' common row is found all the same; beside two of the
+    four, the row is left alone where it would not help."""
     c = _with_row(200, 512, 64, 6, 42, 8.0)
-    c.w[16] *= 1e5                 # one of the four
+    c.w[16] *= 1e5                 # one of the four that it is formed of
     c.z[:, 16] = float("-inf")      # and it is never chosen: its dz is 0
     v, ids = torch.topk(c.z, 6, dim=1)
     c.ids, c.wt = ids.to(torch.int32), torch.softmax(v, 1)
-    assert not _check(c, 0.5, 0.5)[torch.arange(64) != 16].any()
+    others = torch.arange(64) != 16
+    assert _check(c, 0.5, 0.5)[others].all()
+    c.w[16] /= 1e5
+    c.w[16, ::50] += 300.0
+    assert _check(c, 0.5, 0.5)[others].all()
+    c.w[[16, 32]] *= 1e5
+    assert not _check(c, 0.5, 0.5)[torch.arange(64) % 16 != 0].any()
 
 
 def test_one_expert_and_two():
